@@ -80,7 +80,11 @@ typedef enum {
     PARARNN_ERR_UNSUPPORTED = -6   /* e.g. D not a multiple of 8             */
 } pararnn_status;
 
-typedef enum { PARARNN_F32 = 0, PARARNN_BF16 = 1 } pararnn_dtype;
+typedef enum {
+    PARARNN_F32 = 0,
+    PARARNN_BF16 = 1,
+    PARARNN_E4M3 = 2 /* 8 bits: 4 of exponent, 3 of mantissa, largest value 448; where an entry point says so */
+} pararnn_dtype;
 
 /* ABI-identical to cudaStream_t. */
 typedef struct CUstream_st* pararnn_stream_t;
@@ -480,6 +484,145 @@ PARARNN_API pararnn_status pararnn_lstm_step(const void* u, pararnn_dtype u_dtyp
                                              const float* c_prev, const float* h_prev,
                                              float* c_next, float* h_next, int64_t B, int64_t D,
                                              pararnn_stream_t stream);
+
+/* ------------------------------------------------ gated linear recurrence */
+
+/* The linear SSM of "O compromisso que SSMs fizeram" (h_l = A_l h_{l-1} +
+ * B_l x_l, which a parallel scan solves in one pass) with both terms gated by
+ * the input, as a layer of its own: forward over a batch, training gradients,
+ * and one decode step.  Per channel d, with gates u = (r, i, x) and a rate
+ * s_d >= 0 (s = logistic):
+ *   a_t = exp(-s_d s(r_t)),   m_t = sqrt(1 - a_t^2),
+ *   h_t = a_t h_{t-1} + m_t s(i_t) x_t.
+ * Rows are packed: T rows hold n_seq sequences one behind the other.
+ *   u          [T][3][D] gate pre-activations (r, i, x), dtype u_dtype
+ *   rate       [D] fp32, the rates s_d; a negative one gives NaN states
+ *   h0         [n_seq][D] fp32 state before each sequence, or NULL (zeros)
+ *   seq_starts [n_seq + 1] int32, DEVICE: sequence s is the rows from
+ *              seq_starts[s] up to seq_starts[s + 1], not decreasing, within
+ *              0..T; a sequence may be empty.  NULL: equal lengths T / n_seq
+ *              (u is then [n_seq][L][3][D]).  Rows in no sequence are neither
+ *              read for another's result nor written: an output keeps there
+ *              what it held.  (Offsets are held to 0..T on the device; values
+ *              that decrease give undefined results, but no access outside
+ *              the arrays.)
+ *   h          [T][D] fp32 out
+ *   h_last     [n_seq][D] fp32 out, each sequence's last state (h0 where it
+ *              is empty), which glr_step continues from; or NULL
+ * A sequence's result does not depend on what the others hold, NaN and
+ * infinities included.  4-byte alignment suffices for seq_starts.  Outputs
+ * must not overlap inputs or each other.  Asynchronous on `stream`,
+ * capturable in a CUDA graph; a device-side failure (a bounded wait that ran
+ * out) is reported by pararnn_read_result on the same workspace.  Calls that
+ * may run at the same time need workspaces of their own. */
+PARARNN_API size_t pararnn_glr_workspace_size(int64_t T, int64_t n_seq, int64_t D);
+PARARNN_API pararnn_status pararnn_glr_scan(const void* u, pararnn_dtype u_dtype, const float* rate,
+                                            const float* h0, const int32_t* seq_starts, float* h,
+                                            float* h_last, int64_t T, int64_t n_seq, int64_t D,
+                                            void* workspace, size_t workspace_bytes,
+                                            pararnn_stream_t stream);
+
+/* Training gradients through the states h of pararnn_glr_scan: the
+ * reverse-time linear recurrence lambda_t = dh_t + a_{t+1} lambda_{t+1}, with
+ * dh_last added at each sequence's last row.
+ *   dh       [T][D] fp32 dLoss/dh;  dh_last [n_seq][D] fp32 dLoss/dh_last or
+ *            NULL (zeros)
+ *   du       [T][3][D] fp32 out;  drate [D] fp32 out (overwritten; summed in
+ *            a fixed order: the same bits from every run on a device)
+ *   dh0      [n_seq][D] fp32 out (dh_last where a sequence is empty), or NULL
+ * Where a gate is shut (s_d s(r) = 0) the square root has no slope; the terms
+ * through it are 0 there.  Rows in no sequence: as in pararnn_glr_scan. */
+PARARNN_API size_t pararnn_glr_adjoint_workspace_size(int64_t T, int64_t n_seq, int64_t D);
+PARARNN_API pararnn_status pararnn_glr_adjoint(const void* u, pararnn_dtype u_dtype,
+                                               const float* rate, const float* h0,
+                                               const int32_t* seq_starts, const float* h,
+                                               const float* dh, const float* dh_last, float* du,
+                                               float* drate, float* dh0, int64_t T, int64_t n_seq,
+                                               int64_t D, void* workspace, size_t workspace_bytes,
+                                               pararnn_stream_t stream);
+
+/* One step for B sequences (see pararnn_gru_step): u [B][3][D], h_prev [B][D]
+ * or NULL (zeros), h_next [B][D], which may be h_prev itself. */
+PARARNN_API pararnn_status pararnn_glr_step(const void* u, pararnn_dtype u_dtype, const float* rate,
+                                            const float* h_prev, float* h_next, int64_t B, int64_t D,
+                                            pararnn_stream_t stream);
+
+/* ------------------------------------------------------------- RMS norm */
+
+/* The norm in front of a layer's projection, with the residual's addition
+ * before it and, where wanted, an 8-bit output for pararnn_fp8_project:
+ *   v = x + residual (in fp32),  sum = v rounded to sum_dtype,
+ *   rstd = 1 / sqrt(mean over D of v^2 + eps),  y = v rstd w.
+ *   x        [T][D] x_dtype (fp32 or bf16)
+ *   residual [T][D] sum_dtype (fp32 or bf16), or NULL (v = x)
+ *   w        [D] fp32;  eps >= 0
+ *   sum      [T][D] sum_dtype out, or NULL; may be residual itself (in place)
+ *   y        [T][D] y_dtype out: fp32, bf16 or e4m3
+ *   y_scale  [T][ceil(D/128)] fp32 out for e4m3 (else ignored): per row and
+ *            block of 128 columns max(largest |y| / 448, 2^-126);
+ *            y ~ e4m3 value x scale.  A block that holds NaN or infinity
+ *            stands for NaN throughout.
+ *   rstd     [T] fp32 out for the adjoint, or NULL
+ * y and the scales come from the unrounded v.  D a multiple of 8 (16 for
+ * e4m3) and at most 16384, else UNSUPPORTED.  Other overlaps of outputs are
+ * refused.  Asynchronous on `stream`, no workspace. */
+PARARNN_API pararnn_status pararnn_rms_norm(const void* x, pararnn_dtype x_dtype, const void* residual,
+                                            pararnn_dtype sum_dtype, const float* w, float eps,
+                                            void* sum, void* y, pararnn_dtype y_dtype,
+                                            float* y_scale, float* rstd, int64_t T, int64_t D,
+                                            pararnn_stream_t stream);
+
+/* Its gradients, with n = sum rstd and g = dy w:
+ *   dx = dsum + rstd (g - n mean(g n)),   dw = sum over rows of dy n.
+ *   dy    [T][D] dy_dtype (fp32 or bf16): dLoss/dy (for an 8-bit y: of the
+ *         values that it stands for, the rounding taken as the identity)
+ *   sum   [T][D] sum_dtype, rstd [T]: from the forward pass (sum is x where
+ *         there was no residual)
+ *   dsum  [T][D] sum_dtype, the gradient that reaches sum from elsewhere, or
+ *         NULL (zeros)
+ *   dx    [T][D] sum_dtype out, the gradient of x and of residual alike; may
+ *         be dsum itself;  dw [D] fp32 out (overwritten, fixed order) */
+PARARNN_API size_t pararnn_rms_norm_adjoint_workspace_size(int64_t T, int64_t D);
+PARARNN_API pararnn_status pararnn_rms_norm_adjoint(const void* dy, pararnn_dtype dy_dtype,
+                                                    const void* sum, pararnn_dtype sum_dtype,
+                                                    const float* w, const float* rstd,
+                                                    const void* dsum, void* dx, float* dw, int64_t T,
+                                                    int64_t D, void* workspace,
+                                                    size_t workspace_bytes, pararnn_stream_t stream);
+
+/* ---------------------------------------------------------- 8-bit product */
+
+/* e4m3 values with an fp32 scale for each block of 128 columns of block_rows
+ * rows (1: activations; 128: weights): scale = max(largest |x| / 448, 2^-126),
+ * q = x / scale rounded to nearest even.  Blocks at the edges may be short.
+ *   x [M][K] fp32 or bf16;  q [M][K] e4m3 out;
+ *   scale [ceil(M/block_rows)][ceil(K/128)] fp32 out
+ * K a multiple of 16 (else UNSUPPORTED).  A block that holds NaN or infinity
+ * stands for NaN throughout.  Asynchronous on `stream`. */
+PARARNN_API pararnn_status pararnn_fp8_quantize(const void* x, pararnn_dtype x_dtype, int block_rows,
+                                                void* q, float* scale, int64_t M, int64_t K,
+                                                pararnn_stream_t stream);
+
+/* The input projection with 8-bit operands (see pararnn_gru_project_solve for
+ * the bf16 one): on the tensor cores,
+ *   u[m][n] = sum over blocks b of 128 columns of
+ *             x_scale[m][b] w_scale[n / 128][b] (x[m] . w[n] over block b)
+ *             + bias[n],
+ * each block's product and the sum over blocks in fp32, rounded once.
+ *   x       [M][K] e4m3, x_scale [M][ceil(K/128)] fp32 (pararnn_rms_norm, or
+ *           pararnn_fp8_quantize with block_rows 1)
+ *   w       [N][K] e4m3, w_scale [ceil(N/128)][ceil(K/128)] fp32
+ *           (pararnn_fp8_quantize with block_rows 128); for a layer of G
+ *           gates N = G D, the layout of a linear layer's weight
+ *   bias    [N] fp32 or NULL
+ *   u       [M][N] fp32 or bf16 out: the gates [M][G][D] of the solves, the
+ *           scans and the decode steps
+ * K a multiple of 16, N a multiple of 8 (else UNSUPPORTED).  No workspace;
+ * asynchronous on `stream`. */
+PARARNN_API pararnn_status pararnn_fp8_project(const void* x, const float* x_scale, const void* w,
+                                               const float* w_scale, const float* bias, void* u,
+                                               pararnn_dtype u_dtype, int64_t M, int64_t N, int64_t K,
+                                               pararnn_stream_t stream);
 
 /* ------------------------------------------------------------- baselines */
 

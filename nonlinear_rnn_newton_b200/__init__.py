@@ -21,6 +21,13 @@ __all__ = [
     "pararnn_cell_solve",
     "pararnn_cell_solve_async",
     "pararnn_cell_workspace_size",
+    "pararnn_fp8_project",
+    "pararnn_fp8_quantize",
+    "pararnn_glr_adjoint",
+    "pararnn_glr_adjoint_workspace_size",
+    "pararnn_glr_scan",
+    "pararnn_glr_step",
+    "pararnn_glr_workspace_size",
     "pararnn_gru_adjoint",
     "pararnn_gru_adjoint_workspace_size",
     "pararnn_gru_segment_pass",
@@ -53,6 +60,9 @@ __all__ = [
     "pararnn_gru_project_solve_async",
     "pararnn_segment_fold_workspace_size",
     "pararnn_read_result",
+    "pararnn_rms_norm",
+    "pararnn_rms_norm_adjoint",
+    "pararnn_rms_norm_adjoint_workspace_size",
     "pararnn_selftest_wait_timeout",
 ]
 

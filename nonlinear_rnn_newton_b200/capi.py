@@ -26,6 +26,7 @@ ERR_UNSUPPORTED = -6
 
 F32 = 0
 BF16 = 1
+E4M3 = 2
 
 
 class PararnnError(RuntimeError):
@@ -107,6 +108,18 @@ SIGNATURES = {
     "pararnn_gru_step": (_st, [_vp, _st, _vp, _vp, _vp, _i64, _i64, _vp]),
     "pararnn_lstm_step": (_st, [_vp, _st, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp]),
     "pararnn_linear_scan": (_st, [_vp, _st, _vp, _vp, _i64, _i64, _i64, _vp, ctypes.c_size_t, _vp]),
+    "pararnn_glr_workspace_size": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "pararnn_glr_adjoint_workspace_size": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "pararnn_glr_scan": (_st, [_vp, _st, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, ctypes.c_size_t, _vp]),
+    "pararnn_glr_adjoint": (_st, [_vp, _st, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp,
+                                  ctypes.c_size_t, _vp]),
+    "pararnn_glr_step": (_st, [_vp, _st, _vp, _vp, _vp, _i64, _i64, _vp]),
+    "pararnn_rms_norm": (_st, [_vp, _st, _vp, _st, _vp, ctypes.c_float, _vp, _vp, _st, _vp, _vp, _i64, _i64, _vp]),
+    "pararnn_rms_norm_adjoint_workspace_size": (ctypes.c_size_t, [_i64, _i64]),
+    "pararnn_rms_norm_adjoint": (_st, [_vp, _st, _vp, _st, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, ctypes.c_size_t,
+                                       _vp]),
+    "pararnn_fp8_quantize": (_st, [_vp, _st, ctypes.c_int, _vp, _vp, _i64, _i64, _vp]),
+    "pararnn_fp8_project": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _st, _i64, _i64, _i64, _vp]),
     "pararnn_status_string": (ctypes.c_char_p, [_st]),
     "pararnn_last_error": (ctypes.c_char_p, []),
     "pararnn_version": (ctypes.c_char_p, []),
@@ -693,3 +706,249 @@ def pararnn_selftest_wait_timeout(which, limit_ns, workspace, stream=None):
     """Returns the status (ERR_TIMEOUT expected)."""
     return int(lib.pararnn_selftest_wait_timeout(int(which), int(limit_ns), _ptr(workspace),
                                                  workspace.numel(), _stream(workspace.device, stream)))
+
+
+# ------------------------------------------- layer operators (see pararnn.h)
+
+_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
+
+
+def _code(t, name, allowed):
+    dtype = t if isinstance(t, torch.dtype) else t.dtype
+    if dtype not in allowed:
+        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in allowed)}, got {dtype}")
+    return _CODES[dtype]
+
+
+_WIDE = (torch.float32, torch.bfloat16)
+
+
+def _run(fn, dev, stream, *args):
+    """Call fn(*args, stream) with `dev` current; raises unless it returns OK."""
+    if dev.type != "cuda":
+        raise ValueError(f"device tensors are needed, got one on {dev}")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(dev, stream))
+    else:
+        st = fn(*args, _stream(dev, stream))
+    _check(st, allow=(OK,))
+
+
+def pararnn_glr_workspace_size(T, n_seq, D):
+    return int(lib.pararnn_glr_workspace_size(T, n_seq, D))
+
+
+def pararnn_glr_adjoint_workspace_size(T, n_seq, D):
+    return int(lib.pararnn_glr_adjoint_workspace_size(T, n_seq, D))
+
+
+def _glr_args(u, rate, h0, seq_starts):
+    """(rows' shape, T, n_seq, D) of a call on u [B,L,3,D], or on packed rows
+    u [T,3,D] with seq_starts [n_seq + 1]."""
+    if u.dim() != (4 if seq_starts is None else 3) or u.shape[-2] != 3:
+        raise ValueError("u must be [B,L,3,D], or [T,3,D] with seq_starts; got shape "
+                         f"{tuple(u.shape)} {'with' if seq_starts is not None else 'without'} seq_starts")
+    _code(u, "u", _WIDE)
+    if not u.is_contiguous():
+        raise ValueError("u must be contiguous")
+    D = u.shape[-1]
+    if seq_starts is None:
+        n_seq, T = u.shape[0], u.shape[0] * u.shape[1]
+    else:
+        if seq_starts.dim() != 1 or seq_starts.numel() < 2:
+            raise ValueError("seq_starts must be [n_seq + 1]")
+        n_seq, T = seq_starts.numel() - 1, u.shape[0]
+        _need(seq_starts, "seq_starts", (n_seq + 1,), dtype=torch.int32, device=u.device)
+    _need(rate, "rate", (D,), device=u.device)
+    _need(h0, "h0", (n_seq, D), device=u.device)
+    return tuple(u.shape[:-2]) + (D,), T, n_seq, D
+
+
+def _ws_args(ws):
+    return _ptr(ws), ws.numel() * ws.element_size()
+
+
+def pararnn_glr_scan(u, rate, h0=None, seq_starts=None, h=None, h_last=None, want_last=True, workspace=None,
+                     stream=None):
+    """Gated linear recurrence over a batch: u [B,L,3,D] (or packed rows
+    [T,3,D] with seq_starts [n_seq + 1] int32 on the device), bf16/fp32, gates
+    (r, i, x); rate [D] fp32; h0 [n_seq,D] or None.  Returns (h [B,L,D] or
+    [T,D], h_last [n_seq,D] or None).  Rows in no sequence are not written: in
+    an h made here they hold anything.  Asynchronous on the stream."""
+    shape, T, n_seq, D = _glr_args(u, rate, h0, seq_starts)
+    dev = u.device
+    if h is None:
+        h = torch.empty(shape, dtype=torch.float32, device=dev)
+    if h_last is None and want_last:
+        h_last = torch.empty((n_seq, D), dtype=torch.float32, device=dev)
+    _need(h, "h", shape, device=dev)
+    _need(h_last, "h_last", (n_seq, D), device=dev)
+    ws = _workspace(lib.pararnn_glr_workspace_size(T, n_seq, D), dev, workspace)
+    _run(lib.pararnn_glr_scan, dev, stream, _ptr(u), _dtype_code(u), _ptr(rate), _ptr(h0), _ptr(seq_starts), _ptr(h),
+         _ptr(h_last), T, n_seq, D, *_ws_args(ws))
+    return h, h_last
+
+
+def pararnn_glr_adjoint(u, rate, h0, h, dh, dh_last=None, seq_starts=None, du=None, drate=None, dh0=None,
+                        want_dh0=True, workspace=None, stream=None):
+    """Gradients of pararnn_glr_scan at its states h, from dh (and dh_last or
+    None).  Returns (du as u in fp32, drate [D], dh0 [n_seq,D] or None).
+    Asynchronous on the stream."""
+    shape, T, n_seq, D = _glr_args(u, rate, h0, seq_starts)
+    dev = u.device
+    if du is None:
+        du = torch.empty(u.shape, dtype=torch.float32, device=dev)
+    if drate is None:
+        drate = torch.empty((D,), dtype=torch.float32, device=dev)
+    if dh0 is None and want_dh0:
+        dh0 = torch.empty((n_seq, D), dtype=torch.float32, device=dev)
+    for t, n, s in ((h, "h", shape), (dh, "dh", shape), (dh_last, "dh_last", (n_seq, D)), (du, "du", u.shape),
+                    (drate, "drate", (D,)), (dh0, "dh0", (n_seq, D))):
+        _need(t, n, s, device=dev)
+    ws = _workspace(lib.pararnn_glr_adjoint_workspace_size(T, n_seq, D), dev, workspace)
+    _run(lib.pararnn_glr_adjoint, dev, stream, _ptr(u), _dtype_code(u), _ptr(rate), _ptr(h0), _ptr(seq_starts),
+         _ptr(h), _ptr(dh), _ptr(dh_last), _ptr(du), _ptr(drate), _ptr(dh0), T, n_seq, D, *_ws_args(ws))
+    return du, drate, dh0
+
+
+def pararnn_glr_step(u, rate, h_prev=None, h_next=None, stream=None):
+    """One step for B sequences: u [B,3,D], h_prev [B,D] (None = zeros).
+    h_next may be h_prev itself (in place); a new tensor if None."""
+    if u.dim() != 3 or u.shape[1] != 3:
+        raise ValueError(f"u must be [B,3,D], got shape {tuple(u.shape)}")
+    B, _, D = u.shape
+    _need(u, "u", (B, 3, D), dtype=u.dtype)
+    _need(rate, "rate", (D,), device=u.device)
+    _need(h_prev, "h_prev", (B, D), device=u.device)
+    if h_next is None:
+        h_next = torch.empty((B, D), dtype=torch.float32, device=u.device)
+    _need(h_next, "h_next", (B, D), device=u.device)
+    _run(lib.pararnn_glr_step, u.device, stream, _ptr(u), _dtype_code(u), _ptr(rate), _ptr(h_prev), _ptr(h_next), B, D)
+    return h_next
+
+
+def _rows(t, name):
+    if t.dim() < 2:
+        raise ValueError(f"{name} must have at least two dimensions")
+    return t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1]
+
+
+def pararnn_rms_norm(x, w, residual=None, eps=1e-6, out_dtype=torch.bfloat16, sum=None, y=None, y_scale=None,
+                     rstd=None, stream=None):
+    """RMS norm of x + residual: x [..., D] bf16/fp32, w [D] fp32, residual as
+    x in bf16/fp32 or None.  Returns (y [..., D] in out_dtype (fp32, bf16 or
+    float8_e4m3fn), y_scale [..., ceil(D/128)] for 8 bits else None, sum in
+    the residual's type (None without a residual), rstd [...]).  sum may be
+    the residual itself (in place)."""
+    T, D = _rows(x, "x")
+    dev, shape = x.device, tuple(x.shape)
+    yc = _code(out_dtype, "out_dtype", tuple(_CODES))
+    _code(x, "x", _WIDE)
+    _need(x, "x", shape, dtype=x.dtype)
+    _need(w, "w", (D,), device=dev)
+    if residual is not None:
+        rc = _code(residual, "residual", _WIDE)
+        _need(residual, "residual", shape, dtype=residual.dtype, device=dev)
+        if sum is None:
+            sum = torch.empty_like(residual)
+        _need(sum, "sum", shape, dtype=residual.dtype, device=dev)
+    else:
+        if sum is not None:
+            raise ValueError("sum is an output of a call with a residual")
+        rc = F32
+    if y is None:
+        y = torch.empty(shape, dtype=out_dtype, device=dev)
+    _need(y, "y", shape, dtype=out_dtype, device=dev)
+    if yc == E4M3:
+        blocks = shape[:-1] + ((D + 127) // 128,)
+        if y_scale is None:
+            y_scale = torch.empty(blocks, dtype=torch.float32, device=dev)
+        _need(y_scale, "y_scale", blocks, device=dev)
+    elif y_scale is not None:
+        raise ValueError("y_scale is an output of an 8-bit call")
+    if rstd is None:
+        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    _need(rstd, "rstd", shape[:-1], device=dev)
+    _run(lib.pararnn_rms_norm, dev, stream, _ptr(x), _CODES[x.dtype], _ptr(residual), rc, _ptr(w), float(eps),
+         _ptr(sum), _ptr(y), yc, _ptr(y_scale), _ptr(rstd), T, D)
+    return y, y_scale, sum, rstd
+
+
+def pararnn_rms_norm_adjoint_workspace_size(T, D):
+    return int(lib.pararnn_rms_norm_adjoint_workspace_size(T, D))
+
+
+def pararnn_rms_norm_adjoint(dy, sum, w, rstd, dsum=None, dx=None, dw=None, workspace=None, stream=None):
+    """Gradients of pararnn_rms_norm: dy [..., D] bf16/fp32, sum as the forward
+    pass left it (x where there was no residual), rstd, and the gradient dsum
+    that reaches sum from elsewhere (sum's type, or None).  Returns (dx in
+    sum's type, the gradient of x and residual alike, dw [D] fp32).  dx may be
+    dsum itself."""
+    T, D = _rows(sum, "sum")
+    dev, shape = sum.device, tuple(sum.shape)
+    sc, yc = _code(sum, "sum", _WIDE), _code(dy, "dy", _WIDE)
+    _need(sum, "sum", shape, dtype=sum.dtype)
+    _need(dy, "dy", shape, dtype=dy.dtype, device=dev)
+    _need(w, "w", (D,), device=dev)
+    _need(rstd, "rstd", shape[:-1], device=dev)
+    _need(dsum, "dsum", shape, dtype=sum.dtype, device=dev)
+    if dx is None:
+        dx = torch.empty_like(sum)
+    if dw is None:
+        dw = torch.empty((D,), dtype=torch.float32, device=dev)
+    _need(dx, "dx", shape, dtype=sum.dtype, device=dev)
+    _need(dw, "dw", (D,), device=dev)
+    ws = _workspace(lib.pararnn_rms_norm_adjoint_workspace_size(T, D), dev, workspace)
+    _run(lib.pararnn_rms_norm_adjoint, dev, stream, _ptr(dy), yc, _ptr(sum), sc, _ptr(w), _ptr(rstd), _ptr(dsum),
+         _ptr(dx), _ptr(dw), T, D, *_ws_args(ws))
+    return dx, dw
+
+
+def pararnn_fp8_quantize(x, block_rows=1, q=None, scale=None, stream=None):
+    """e4m3 values of x [..., K] (bf16/fp32) and their scales: per row and 128
+    columns (block_rows = 1, scale [..., ceil(K/128)]) or per 128 rows and 128
+    columns (block_rows = 128, x [N,K], scale [ceil(N/128), ceil(K/128)])."""
+    M, K = _rows(x, "x")
+    dev, shape = x.device, tuple(x.shape)
+    xc = _code(x, "x", _WIDE)
+    _need(x, "x", shape, dtype=x.dtype)
+    if block_rows == 1:
+        blocks = shape[:-1] + ((K + 127) // 128,)
+    elif block_rows == 128:
+        if x.dim() != 2:
+            raise ValueError("x must be [N,K] for blocks of 128 rows")
+        blocks = ((M + 127) // 128, (K + 127) // 128)
+    else:
+        raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
+    if q is None:
+        q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+    if scale is None:
+        scale = torch.empty(blocks, dtype=torch.float32, device=dev)
+    _need(q, "q", shape, dtype=torch.float8_e4m3fn, device=dev)
+    _need(scale, "scale", blocks, device=dev)
+    _run(lib.pararnn_fp8_quantize, dev, stream, _ptr(x), xc, block_rows, _ptr(q), _ptr(scale), M, K)
+    return q, scale
+
+
+def pararnn_fp8_project(x, x_scale, w, w_scale, bias=None, out_dtype=torch.bfloat16, u=None, stream=None):
+    """Projection of 8-bit operands: x [..., K] and w [N,K] float8_e4m3fn with
+    their scales (pararnn_rms_norm or pararnn_fp8_quantize), bias [N] fp32 or
+    None.  Returns u [..., N] in out_dtype (bf16 or fp32)."""
+    M, K = _rows(x, "x")
+    dev, shape = x.device, tuple(x.shape)
+    if w.dim() != 2 or w.shape[1] != K:
+        raise ValueError(f"w must be [N,{K}], got {tuple(w.shape)}")
+    N = w.shape[0]
+    uc = _code(out_dtype, "out_dtype", _WIDE)
+    _need(x, "x", shape, dtype=torch.float8_e4m3fn)
+    _need(x_scale, "x_scale", shape[:-1] + ((K + 127) // 128,), device=dev)
+    _need(w, "w", (N, K), dtype=torch.float8_e4m3fn, device=dev)
+    _need(w_scale, "w_scale", ((N + 127) // 128, (K + 127) // 128), device=dev)
+    _need(bias, "bias", (N,), device=dev)
+    if u is None:
+        u = torch.empty(shape[:-1] + (N,), dtype=out_dtype, device=dev)
+    _need(u, "u", shape[:-1] + (N,), dtype=out_dtype, device=dev)
+    _run(lib.pararnn_fp8_project, dev, stream, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(u), uc,
+         M, N, K)
+    return u

@@ -1,0 +1,435 @@
+// Host side of the layer operators: the gated linear recurrence, the RMS norm
+// and the 8-bit product -- argument checks, workspace layouts and launches.
+// Included at the end of pararnn_capi.cu: it uses that file's helpers (fail,
+// TRY, check_ptr, the tensor-map encoder, resident_grid, ...).
+#pragma once
+
+#include "fp8.cuh"
+#include "glr.cuh"
+#include "norm.cuh"
+
+namespace {
+
+constexpr double kMaxBytes = 1099511627776.0;  // 2^40
+
+size_t dtype_bytes(pararnn_dtype dt) { return dt == PARARNN_F32 ? 4 : dt == PARARNN_BF16 ? 2 : 1; }
+
+pararnn_status check_wide_dtype(pararnn_dtype dt, const char* name)
+{
+    if (dt != PARARNN_F32 && dt != PARARNN_BF16)
+        return fail(PARARNN_ERR_INVALID_ARG, "%s must be PARARNN_F32 or PARARNN_BF16 (got %d)", name, int(dt));
+    return PARARNN_OK;
+}
+
+// do the byte ranges [x, x + nx) and [y, y + ny) meet?
+bool meet(const void* x, size_t nx, const void* y, size_t ny)
+{
+    if (!x || !y) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return a < b + ny && b < a + nx;
+}
+
+struct Range {
+    const char* name;
+    const void* p;
+    size_t bytes;
+};
+
+// no output may meet an input or another output; {in, out} pairs for which
+// `out` may be the very buffer of `in` are listed as equal pointers allowed
+template <int NI, int NO>
+pararnn_status check_apart(const Range (&in)[NI], const Range (&out)[NO], const void* in_place)
+{
+    for (int i = 0; i < NO; ++i) {
+        for (int j = 0; j < NI; ++j)
+            if (meet(in[j].p, in[j].bytes, out[i].p, out[i].bytes) &&
+                !(in_place && out[i].p == in_place && in[j].p == in_place && in[j].bytes == out[i].bytes))
+                return fail(PARARNN_ERR_INVALID_ARG, "output %s overlaps input %s", out[i].name, in[j].name);
+        for (int j = 0; j < i; ++j)
+            if (meet(out[j].p, out[j].bytes, out[i].p, out[i].bytes))
+                return fail(PARARNN_ERR_INVALID_ARG, "outputs %s and %s overlap", out[j].name, out[i].name);
+    }
+    return PARARNN_OK;
+}
+
+pararnn_status launched()
+{
+    CUDA_TRY(cudaGetLastError());
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return PARARNN_OK;
+}
+
+// ------------------------------------------------ gated linear recurrence
+
+pararnn_status glr_shape(long long T, long long n_seq, long long D, const void* starts)
+{
+    if (T < 1 || n_seq < 1 || D < 1)
+        return fail(PARARNN_ERR_INVALID_ARG, "T, n_seq, D must be >= 1 (got %lld, %lld, %lld)", T, n_seq, D);
+    if (D % 8 != 0) return fail(PARARNN_ERR_UNSUPPORTED, "D must be a multiple of 8 (got %lld)", D);
+    if (T > INT_MAX / 2 || n_seq > INT_MAX / 2 || D > INT_MAX / 2)
+        return fail(PARARNN_ERR_INVALID_ARG, "dimension too large");
+    if ((double)T * (double)D * 12.0 >= kMaxBytes || (double)n_seq * (double)D * 4.0 >= kMaxBytes)
+        return fail(PARARNN_ERR_INVALID_ARG, "T*D or n_seq*D too large (arrays must stay below 2^40 bytes)");
+    if (!starts && T % n_seq != 0)
+        return fail(PARARNN_ERR_INVALID_ARG, "without seq_starts T must be a multiple of n_seq (got %lld, %lld)", T, n_seq);
+    return PARARNN_OK;
+}
+
+pararnn_status check_starts(const void* starts)
+{
+    if (starts && (reinterpret_cast<uintptr_t>(starts) & 3u) != 0)
+        return fail(PARARNN_ERR_INVALID_ARG, "seq_starts is not 4-byte aligned");
+    return PARARNN_OK;
+}
+
+size_t glr_ws_bytes(bool adjoint, long long T, long long n_seq, long long D)
+{
+    if (T < 1 || n_seq < 1 || D < 1 || D % 8 != 0 || T > INT_MAX / 2 || n_seq > INT_MAX / 2 || D > INT_MAX / 2 ||
+        (double)T * (double)D * 12.0 >= kMaxBytes || (double)n_seq * (double)D * 4.0 >= kMaxBytes)
+        return 0;
+    return adjoint ? align256(size_t(n_seq) * D * 4) : 256;
+}
+
+template <class UT>
+pararnn_status launch_glr_scan(const UT* u, const float* rate, const float* h0, const int* starts, float* h,
+                               float* h_last, long long T, long long n_seq, long long D, cudaStream_t st)
+{
+    glr_scan_seq_kernel<UT><<<unsigned((n_seq * D + 63) / 64), 64, 0, st>>>(u, rate, h0, starts, h, h_last, T, n_seq, D);
+    return launched();
+}
+
+template <class UT>
+pararnn_status launch_glr_adjoint(const UT* u, const float* rate, const float* h0, const int* starts, const float* h,
+                                  const float* dh, const float* dh_last, float* du, float* drate, float* dh0,
+                                  long long T, long long n_seq, long long D, void* ws, cudaStream_t st)
+{
+    float* part = static_cast<float*>(ws);
+    glr_adjoint_seq_kernel<UT><<<unsigned((n_seq * D + 63) / 64), 64, 0, st>>>(u, rate, h0, starts, h, dh, dh_last, du,
+                                                                              dh0, part, T, n_seq, D);
+    TRY(launched());
+    column_sum_kernel<<<unsigned((D + 31) / 32), 256, 0, st>>>(part, drate, n_seq, D);
+    return launched();
+}
+
+// --------------------------------------------------------------- RMS norm
+
+struct NormShape {
+    int tpr, nv, threads, rows;
+};
+
+pararnn_status norm_shape(long long T, long long D, NormShape* s)
+{
+    if (T < 1 || D < 1) return fail(PARARNN_ERR_INVALID_ARG, "T, D must be >= 1 (got %lld, %lld)", T, D);
+    if (D % 8 != 0) return fail(PARARNN_ERR_UNSUPPORTED, "D must be a multiple of 8 (got %lld)", D);
+    if (D > kNormMaxD) return fail(PARARNN_ERR_UNSUPPORTED, "D must be at most %lld (got %lld)", kNormMaxD, D);
+    if (T > INT_MAX / 2 || (double)T * (double)D * 4.0 >= kMaxBytes)
+        return fail(PARARNN_ERR_INVALID_ARG, "T too large (got %lld)", T);
+    const int d8 = int(D / 8);
+    // the fewest threads a row that keep it within kNormVectors vectors each
+    int tpr = 32;
+    while (tpr * kNormVectors < d8) tpr *= 2;
+    // with few rows the chip is far from full: spread each over more threads
+    while (tpr < kNormThreads && tpr < d8 && T * tpr < 148 * 512) tpr *= 2;
+    s->tpr = tpr;
+    s->nv = 1;
+    while (s->nv * tpr < d8) s->nv *= 2;
+    s->threads = std::max(tpr, 128);
+    s->rows = s->threads / tpr;
+    return PARARNN_OK;
+}
+
+int norm_adjoint_grid(long long T, const NormShape& s) { return int(std::min<long long>((T + s.rows - 1) / s.rows, 148 * 4)); }
+
+template <class XT, class RT>
+pararnn_status launch_norm(const NormParams& p, const NormShape& s, cudaStream_t st)
+{
+    const unsigned grid = unsigned((p.T + s.rows - 1) / s.rows);
+    switch (s.nv) {
+    case 1: rms_norm_kernel<XT, RT, 1><<<grid, s.threads, 0, st>>>(p); break;
+    case 2: rms_norm_kernel<XT, RT, 2><<<grid, s.threads, 0, st>>>(p); break;
+    default: rms_norm_kernel<XT, RT, 4><<<grid, s.threads, 0, st>>>(p); break;
+    }
+    return launched();
+}
+
+template <class YT, class VT>
+pararnn_status launch_norm_adjoint(const NormAdjParams& p, const NormShape& s, cudaStream_t st)
+{
+    const unsigned grid = unsigned(norm_adjoint_grid(p.T, s));
+    const size_t smem = s.rows > 1 ? size_t(s.rows) * p.D * 4 : 0;  // at most 4 rows of 2048 columns
+    switch (s.nv) {
+    case 1: rms_norm_adjoint_kernel<YT, VT, 1><<<grid, s.threads, smem, st>>>(p); break;
+    case 2: rms_norm_adjoint_kernel<YT, VT, 2><<<grid, s.threads, smem, st>>>(p); break;
+    default: rms_norm_adjoint_kernel<YT, VT, 4><<<grid, s.threads, smem, st>>>(p); break;
+    }
+    return launched();
+}
+
+// ----------------------------------------------------------- 8-bit product
+
+pararnn_status fp8_dims(long long M, long long N, long long K)
+{
+    if (M < 1 || N < 1 || K < 1)
+        return fail(PARARNN_ERR_INVALID_ARG, "M, N, K must be >= 1 (got %lld, %lld, %lld)", M, N, K);
+    if (K % 16 != 0) return fail(PARARNN_ERR_UNSUPPORTED, "K must be a multiple of 16 (got %lld)", K);
+    if (N % 8 != 0) return fail(PARARNN_ERR_UNSUPPORTED, "N must be a multiple of 8 (got %lld)", N);
+    if (M > INT_MAX / 2 || N > INT_MAX / 2 || K > INT_MAX / 2 || (double)M * (double)K * 4.0 >= kMaxBytes ||
+        (double)M * (double)N * 4.0 >= kMaxBytes || (double)N * (double)K * 4.0 >= kMaxBytes)
+        return fail(PARARNN_ERR_INVALID_ARG, "dimension too large");
+    return PARARNN_OK;
+}
+
+long long blocks128(long long n) { return (n + 127) / 128; }
+
+}  // namespace
+
+extern "C" {
+
+size_t pararnn_glr_workspace_size(int64_t T, int64_t n_seq, int64_t D) { return glr_ws_bytes(false, T, n_seq, D); }
+size_t pararnn_glr_adjoint_workspace_size(int64_t T, int64_t n_seq, int64_t D) { return glr_ws_bytes(true, T, n_seq, D); }
+
+pararnn_status pararnn_glr_scan(const void* u, pararnn_dtype u_dtype, const float* rate, const float* h0,
+                                const int32_t* seq_starts, float* h, float* h_last, int64_t T, int64_t n_seq, int64_t D,
+                                void* workspace, size_t workspace_bytes, pararnn_stream_t stream)
+{
+    t_err[0] = '\0';
+    TRY(check_wide_dtype(u_dtype, "u_dtype"));
+    TRY(check_ptr(u, "u", true));
+    TRY(check_ptr(rate, "rate", true));
+    TRY(check_ptr(h0, "h0", false));
+    TRY(check_starts(seq_starts));
+    TRY(check_ptr(h, "h", true));
+    TRY(check_ptr(h_last, "h_last", false));
+    TRY(glr_shape(T, n_seq, D, seq_starts));
+    const size_t rows = size_t(T) * D, ends = size_t(n_seq) * D * 4;
+    TRY((check_apart<4, 2>({{"u", u, rows * 3 * dtype_bytes(u_dtype)}, {"rate", rate, size_t(D) * 4}, {"h0", h0, ends},
+                           {"seq_starts", seq_starts, size_t(n_seq + 1) * 4}},
+                          {{"h", h, rows * 4}, {"h_last", h_last, ends}}, nullptr)));
+    TRY(check_workspace(workspace, workspace_bytes, glr_ws_bytes(false, T, n_seq, D)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (u_dtype == PARARNN_BF16)
+        return launch_glr_scan(static_cast<const uint16_t*>(u), rate, h0, seq_starts, h, h_last, T, n_seq, D, st);
+    return launch_glr_scan(static_cast<const float*>(u), rate, h0, seq_starts, h, h_last, T, n_seq, D, st);
+}
+
+pararnn_status pararnn_glr_adjoint(const void* u, pararnn_dtype u_dtype, const float* rate, const float* h0,
+                                   const int32_t* seq_starts, const float* h, const float* dh, const float* dh_last,
+                                   float* du, float* drate, float* dh0, int64_t T, int64_t n_seq, int64_t D,
+                                   void* workspace, size_t workspace_bytes, pararnn_stream_t stream)
+{
+    t_err[0] = '\0';
+    TRY(check_wide_dtype(u_dtype, "u_dtype"));
+    TRY(check_ptr(u, "u", true));
+    TRY(check_ptr(rate, "rate", true));
+    TRY(check_ptr(h0, "h0", false));
+    TRY(check_starts(seq_starts));
+    TRY(check_ptr(h, "h", true));
+    TRY(check_ptr(dh, "dh", true));
+    TRY(check_ptr(dh_last, "dh_last", false));
+    TRY(check_ptr(du, "du", true));
+    TRY(check_ptr(drate, "drate", true));
+    TRY(check_ptr(dh0, "dh0", false));
+    TRY(glr_shape(T, n_seq, D, seq_starts));
+    const size_t rows = size_t(T) * D, ends = size_t(n_seq) * D * 4;
+    TRY((check_apart<7, 3>({{"u", u, rows * 3 * dtype_bytes(u_dtype)}, {"rate", rate, size_t(D) * 4}, {"h0", h0, ends},
+                           {"seq_starts", seq_starts, size_t(n_seq + 1) * 4}, {"h", h, rows * 4}, {"dh", dh, rows * 4},
+                           {"dh_last", dh_last, ends}},
+                          {{"du", du, rows * 12}, {"drate", drate, size_t(D) * 4}, {"dh0", dh0, ends}}, nullptr)));
+    TRY(check_workspace(workspace, workspace_bytes, glr_ws_bytes(true, T, n_seq, D)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (u_dtype == PARARNN_BF16)
+        return launch_glr_adjoint(static_cast<const uint16_t*>(u), rate, h0, seq_starts, h, dh, dh_last, du, drate, dh0,
+                                  T, n_seq, D, workspace, st);
+    return launch_glr_adjoint(static_cast<const float*>(u), rate, h0, seq_starts, h, dh, dh_last, du, drate, dh0, T,
+                              n_seq, D, workspace, st);
+}
+
+pararnn_status pararnn_glr_step(const void* u, pararnn_dtype u_dtype, const float* rate, const float* h_prev,
+                                float* h_next, int64_t B, int64_t D, pararnn_stream_t stream)
+{
+    t_err[0] = '\0';
+    TRY(check_wide_dtype(u_dtype, "u_dtype"));
+    TRY(check_ptr(u, "u", true));
+    TRY(check_ptr(rate, "rate", true));
+    TRY(check_ptr(h_prev, "h_prev", false));
+    TRY(check_ptr(h_next, "h_next", true));
+    TRY(check_step_shape(B, D));
+    const size_t n = size_t(B) * D;
+    TRY((check_apart<3, 1>({{"u", u, n * 3 * dtype_bytes(u_dtype)}, {"rate", rate, size_t(D) * 4}, {"h_prev", h_prev, n * 4}},
+                          {{"h_next", h_next, n * 4}}, h_prev)));
+    const unsigned grid = unsigned((n / 4 + 255) / 256);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (u_dtype == PARARNN_BF16)
+        glr_step_kernel<uint16_t><<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(u), rate, h_prev, h_next, B, D);
+    else
+        glr_step_kernel<float><<<grid, 256, 0, st>>>(static_cast<const float*>(u), rate, h_prev, h_next, B, D);
+    return launched();
+}
+
+pararnn_status pararnn_rms_norm(const void* x, pararnn_dtype x_dtype, const void* residual, pararnn_dtype sum_dtype,
+                                const float* w, float eps, void* sum, void* y, pararnn_dtype y_dtype, float* y_scale,
+                                float* rstd, int64_t T, int64_t D, pararnn_stream_t stream)
+{
+    t_err[0] = '\0';
+    TRY(check_wide_dtype(x_dtype, "x_dtype"));
+    TRY(check_wide_dtype(sum_dtype, "sum_dtype"));
+    if (y_dtype != PARARNN_F32 && y_dtype != PARARNN_BF16 && y_dtype != PARARNN_E4M3)
+        return fail(PARARNN_ERR_INVALID_ARG, "unknown y dtype %d", int(y_dtype));
+    TRY(check_ptr(x, "x", true));
+    TRY(check_ptr(residual, "residual", false));
+    TRY(check_ptr(w, "w", true));
+    TRY(check_ptr(sum, "sum", false));
+    TRY(check_ptr(y, "y", true));
+    TRY(check_ptr(y_scale, "y_scale", y_dtype == PARARNN_E4M3));
+    TRY(check_ptr(rstd, "rstd", false));
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(PARARNN_ERR_INVALID_ARG, "eps must be >= 0 and finite");
+    NormShape s;
+    TRY(norm_shape(T, D, &s));
+    if (y_dtype == PARARNN_E4M3 && D % 16 != 0)
+        return fail(PARARNN_ERR_UNSUPPORTED, "D must be a multiple of 16 for an 8-bit output (got %lld)", (long long)D);
+    const size_t n = size_t(T) * D;
+    TRY((check_apart<3, 4>({{"x", x, n * dtype_bytes(x_dtype)}, {"residual", residual, n * dtype_bytes(sum_dtype)},
+                           {"w", w, size_t(D) * 4}},
+                          {{"sum", sum, n * dtype_bytes(sum_dtype)}, {"y", y, n * dtype_bytes(y_dtype)},
+                           {"y_scale", y_dtype == PARARNN_E4M3 ? y_scale : nullptr, size_t(T) * blocks128(D) * 4},
+                           {"rstd", rstd, size_t(T) * 4}},
+                          residual && residual == sum ? residual : nullptr)));
+    NormParams p;
+    p.x = x;
+    p.res = residual;
+    p.w = w;
+    p.sum = sum;
+    p.y = y;
+    p.scale = y_scale;
+    p.rstd = rstd;
+    p.T = T;
+    p.D = D;
+    p.eps = eps;
+    p.tpr = s.tpr;
+    p.sum_bf16 = sum_dtype == PARARNN_BF16;
+    p.y_dtype = y_dtype;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (x_dtype == PARARNN_BF16) {
+        if (!residual) return launch_norm<uint16_t, void>(p, s, st);
+        return p.sum_bf16 ? launch_norm<uint16_t, uint16_t>(p, s, st) : launch_norm<uint16_t, float>(p, s, st);
+    }
+    if (!residual) return launch_norm<float, void>(p, s, st);
+    return p.sum_bf16 ? launch_norm<float, uint16_t>(p, s, st) : launch_norm<float, float>(p, s, st);
+}
+
+size_t pararnn_rms_norm_adjoint_workspace_size(int64_t T, int64_t D)
+{
+    NormShape s;
+    if (norm_shape(T, D, &s) != PARARNN_OK) return 0;
+    return align256(size_t(norm_adjoint_grid(T, s)) * D * 4);
+}
+
+pararnn_status pararnn_rms_norm_adjoint(const void* dy, pararnn_dtype dy_dtype, const void* sum, pararnn_dtype sum_dtype,
+                                        const float* w, const float* rstd, const void* dsum, void* dx, float* dw,
+                                        int64_t T, int64_t D, void* workspace, size_t workspace_bytes,
+                                        pararnn_stream_t stream)
+{
+    t_err[0] = '\0';
+    TRY(check_wide_dtype(dy_dtype, "dy_dtype"));
+    TRY(check_wide_dtype(sum_dtype, "sum_dtype"));
+    TRY(check_ptr(dy, "dy", true));
+    TRY(check_ptr(sum, "sum", true));
+    TRY(check_ptr(w, "w", true));
+    TRY(check_ptr(rstd, "rstd", true));
+    TRY(check_ptr(dsum, "dsum", false));
+    TRY(check_ptr(dx, "dx", true));
+    TRY(check_ptr(dw, "dw", true));
+    NormShape s;
+    TRY(norm_shape(T, D, &s));
+    const size_t n = size_t(T) * D, es = dtype_bytes(sum_dtype);
+    TRY((check_apart<5, 2>({{"dy", dy, n * dtype_bytes(dy_dtype)}, {"sum", sum, n * es}, {"w", w, size_t(D) * 4},
+                           {"rstd", rstd, size_t(T) * 4}, {"dsum", dsum, n * es}},
+                          {{"dx", dx, n * es}, {"dw", dw, size_t(D) * 4}}, dsum && dsum == dx ? dsum : nullptr)));
+    TRY(check_workspace(workspace, workspace_bytes, align256(size_t(norm_adjoint_grid(T, s)) * D * 4)));
+    NormAdjParams p;
+    p.dy = dy;
+    p.v = sum;
+    p.w = w;
+    p.rstd = rstd;
+    p.dv = dsum;
+    p.dx = dx;
+    p.part = static_cast<float*>(workspace);
+    p.T = T;
+    p.D = D;
+    p.tpr = s.tpr;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (dy_dtype == PARARNN_BF16)
+        TRY((sum_dtype == PARARNN_BF16 ? launch_norm_adjoint<uint16_t, uint16_t>(p, s, st)
+                                       : launch_norm_adjoint<uint16_t, float>(p, s, st)));
+    else
+        TRY((sum_dtype == PARARNN_BF16 ? launch_norm_adjoint<float, uint16_t>(p, s, st)
+                                       : launch_norm_adjoint<float, float>(p, s, st)));
+    column_sum_kernel<<<unsigned((D + 31) / 32), 256, 0, st>>>(p.part, dw, norm_adjoint_grid(T, s), D);
+    return launched();
+}
+
+pararnn_status pararnn_fp8_quantize(const void* x, pararnn_dtype x_dtype, int block_rows, void* q, float* scale, int64_t M,
+                                    int64_t K, pararnn_stream_t stream)
+{
+    t_err[0] = '\0';
+    TRY(check_wide_dtype(x_dtype, "x_dtype"));
+    TRY(check_ptr(x, "x", true));
+    TRY(check_ptr(q, "q", true));
+    TRY(check_ptr(scale, "scale", true));
+    if (block_rows != 1 && block_rows != 128)
+        return fail(PARARNN_ERR_INVALID_ARG, "block_rows must be 1 or 128 (got %d)", block_rows);
+    TRY(fp8_dims(M, 8, K));
+    const long long KB = blocks128(K), sets = block_rows == 1 ? (M * KB * 16 + 255) / 256 : blocks128(M) * KB;
+    if (sets > INT_MAX) return fail(PARARNN_ERR_INVALID_ARG, "too many blocks");
+    TRY((check_apart<1, 2>({{"x", x, size_t(M) * K * dtype_bytes(x_dtype)}},
+                          {{"q", q, size_t(M) * K},
+                           {"scale", scale, size_t(block_rows == 1 ? M : blocks128(M)) * KB * 4}}, nullptr)));
+    const unsigned grid = unsigned(sets);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t* out = static_cast<uint8_t*>(q);
+    if (block_rows == 1) {
+        if (x_dtype == PARARNN_BF16) fp8_quantize_rows_kernel<uint16_t><<<grid, 256, 0, st>>>(x, out, scale, M, K, KB);
+        else fp8_quantize_rows_kernel<float><<<grid, 256, 0, st>>>(x, out, scale, M, K, KB);
+    } else {
+        if (x_dtype == PARARNN_BF16) fp8_quantize_blocks_kernel<uint16_t><<<grid, 256, 0, st>>>(x, out, scale, M, K, KB);
+        else fp8_quantize_blocks_kernel<float><<<grid, 256, 0, st>>>(x, out, scale, M, K, KB);
+    }
+    return launched();
+}
+
+pararnn_status pararnn_fp8_project(const void* x, const float* x_scale, const void* w, const float* w_scale,
+                                   const float* bias, void* u, pararnn_dtype u_dtype, int64_t M, int64_t N, int64_t K,
+                                   pararnn_stream_t stream)
+{
+    t_err[0] = '\0';
+    TRY(check_wide_dtype(u_dtype, "u_dtype"));
+    TRY(check_ptr(x, "x", true));
+    TRY(check_ptr(x_scale, "x_scale", true));
+    TRY(check_ptr(w, "w", true));
+    TRY(check_ptr(w_scale, "w_scale", true));
+    TRY(check_ptr(bias, "bias", false));
+    TRY(check_ptr(u, "u", true));
+    TRY(fp8_dims(M, N, K));
+    const long long KB = blocks128(K);
+    TRY((check_apart<5, 1>({{"x", x, size_t(M) * K}, {"x_scale", x_scale, size_t(M) * KB * 4}, {"w", w, size_t(N) * K},
+                           {"w_scale", w_scale, size_t(blocks128(N)) * KB * 4}, {"bias", bias, size_t(N) * 4}},
+                          {{"u", u, size_t(M) * N * dtype_bytes(u_dtype)}}, nullptr)));
+    Fp8Params p;
+    p.x = static_cast<const uint8_t*>(x);
+    p.w = static_cast<const uint8_t*>(w);
+    p.xs = x_scale;
+    p.ws = w_scale;
+    p.bias = bias;
+    p.u = u;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.KB = KB;
+    p.u_bf16 = u_dtype == PARARNN_BF16;
+    if ((M + 63) / 64 > 65535) return fail(PARARNN_ERR_INVALID_ARG, "M too large");
+    fp8_project_kernel<<<dim3(unsigned((N + 63) / 64), unsigned((M + 63) / 64)), 256, 0,
+                         reinterpret_cast<cudaStream_t>(stream)>>>(p);
+    return launched();
+}
+
+}  // extern "C"

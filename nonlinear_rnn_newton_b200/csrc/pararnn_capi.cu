@@ -1449,3 +1449,6 @@ pararnn_status pararnn_selftest_wait_timeout(int which, int64_t limit_ns, void* 
 
 // user-written cells, compiled at run time
 #include "cell_rtc_host.h"
+
+// the gated linear recurrence, the RMS norm and the 8-bit product
+#include "layer_ops_host.h"
