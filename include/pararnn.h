@@ -617,11 +617,14 @@ PARARNN_API pararnn_status pararnn_fp8_quantize(const void* x, pararnn_dtype x_d
  *   bias    [N] fp32 or NULL
  *   u       [M][N] fp32 or bf16 out: the gates [M][G][D] of the solves, the
  *           scans and the decode steps
- * K a multiple of 16, N a multiple of 8 (else UNSUPPORTED).  No workspace;
- * asynchronous on `stream`. */
+ * K a multiple of 16, N a multiple of 8 (else UNSUPPORTED).  Asynchronous on
+ * `stream`; a device-side failure (a bounded wait that ran out) is reported
+ * by pararnn_read_result on the same workspace. */
+PARARNN_API size_t pararnn_fp8_project_workspace_size(int64_t M, int64_t N, int64_t K);
 PARARNN_API pararnn_status pararnn_fp8_project(const void* x, const float* x_scale, const void* w,
                                                const float* w_scale, const float* bias, void* u,
                                                pararnn_dtype u_dtype, int64_t M, int64_t N, int64_t K,
+                                               void* workspace, size_t workspace_bytes,
                                                pararnn_stream_t stream);
 
 /* ------------------------------------------------------------- baselines */

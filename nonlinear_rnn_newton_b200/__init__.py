@@ -22,6 +22,7 @@ __all__ = [
     "pararnn_cell_solve_async",
     "pararnn_cell_workspace_size",
     "pararnn_fp8_project",
+    "pararnn_fp8_project_workspace_size",
     "pararnn_fp8_quantize",
     "pararnn_glr_adjoint",
     "pararnn_glr_adjoint_workspace_size",

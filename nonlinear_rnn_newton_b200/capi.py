@@ -119,7 +119,8 @@ SIGNATURES = {
     "pararnn_rms_norm_adjoint": (_st, [_vp, _st, _vp, _st, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, ctypes.c_size_t,
                                        _vp]),
     "pararnn_fp8_quantize": (_st, [_vp, _st, ctypes.c_int, _vp, _vp, _i64, _i64, _vp]),
-    "pararnn_fp8_project": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _st, _i64, _i64, _i64, _vp]),
+    "pararnn_fp8_project_workspace_size": (ctypes.c_size_t, [_i64, _i64, _i64]),
+    "pararnn_fp8_project": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _st, _i64, _i64, _i64, _vp, ctypes.c_size_t, _vp]),
     "pararnn_status_string": (ctypes.c_char_p, [_st]),
     "pararnn_last_error": (ctypes.c_char_p, []),
     "pararnn_version": (ctypes.c_char_p, []),
@@ -931,7 +932,12 @@ def pararnn_fp8_quantize(x, block_rows=1, q=None, scale=None, stream=None):
     return q, scale
 
 
-def pararnn_fp8_project(x, x_scale, w, w_scale, bias=None, out_dtype=torch.bfloat16, u=None, stream=None):
+def pararnn_fp8_project_workspace_size(M, N, K):
+    return int(lib.pararnn_fp8_project_workspace_size(M, N, K))
+
+
+def pararnn_fp8_project(x, x_scale, w, w_scale, bias=None, out_dtype=torch.bfloat16, u=None, workspace=None,
+                        stream=None):
     """Projection of 8-bit operands: x [..., K] and w [N,K] float8_e4m3fn with
     their scales (pararnn_rms_norm or pararnn_fp8_quantize), bias [N] fp32 or
     None.  Returns u [..., N] in out_dtype (bf16 or fp32)."""
@@ -949,6 +955,7 @@ def pararnn_fp8_project(x, x_scale, w, w_scale, bias=None, out_dtype=torch.bfloa
     if u is None:
         u = torch.empty(shape[:-1] + (N,), dtype=out_dtype, device=dev)
     _need(u, "u", shape[:-1] + (N,), dtype=out_dtype, device=dev)
+    ws = _workspace(lib.pararnn_fp8_project_workspace_size(M, N, K), dev, workspace)
     _run(lib.pararnn_fp8_project, dev, stream, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(u), uc,
-         M, N, K)
+         M, N, K, *_ws_args(ws))
     return u

@@ -181,6 +181,97 @@ pararnn_status fp8_dims(long long M, long long N, long long K)
 
 long long blocks128(long long n) { return (n + 127) / 128; }
 
+// e4m3 [rows][K] -> box [box_rows][128] with the 128-byte swizzle; K a multiple
+// of 16, columns and rows beyond the array read as zeros.
+pararnn_status map_e4m3_sw128(CUtensorMap* m, const void* p, long long rows, long long K, int box_rows)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return fail(PARARNN_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+    cuuint64_t dims[2] = {cuuint64_t(K), cuuint64_t(rows)};
+    cuuint64_t strides[1] = {cuuint64_t(K)};
+    cuuint32_t box[2] = {cuuint32_t(kQK), cuuint32_t(box_rows)};
+    cuuint32_t estr[2] = {1u, 1u};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PARARNN_ERR_CUDA, "cuTensorMapEncodeTiled(8-bit operand) failed: %d", int(r));
+    return PARARNN_OK;
+}
+
+// u [M][N] -> box of 32 rows x 128 bytes with the 128-byte swizzle
+pararnn_status map_sums_sw128(CUtensorMap* m, void* u, long long M, long long N, bool bf16)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return fail(PARARNN_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+    const cuuint64_t es = bf16 ? 2 : 4;
+    cuuint64_t dims[2] = {cuuint64_t(N), cuuint64_t(M)};
+    cuuint64_t strides[1] = {cuuint64_t(N) * es};
+    cuuint32_t box[2] = {cuuint32_t(128 / es), 32u};
+    cuuint32_t estr[2] = {1u, 1u};
+    CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, u, dims, strides,
+                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PARARNN_ERR_CUDA, "cuTensorMapEncodeTiled(output) failed: %d", int(r));
+    return PARARNN_OK;
+}
+
+template <class K>
+pararnn_status launch_clusters(K kern, int grid, int threads, int cluster, size_t smem, cudaStream_t st, void** args)
+{
+    CUDA_TRY(cudaFuncSetAttribute(reinterpret_cast<const void*>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = unsigned(cluster);
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    CUDA_TRY(cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kern), args));
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return PARARNN_OK;
+}
+
+template <int NT>
+pararnn_status launch_narrow(const uint8_t* x, const uint8_t* w, Fp8Params p, int sms, cudaStream_t st)
+{
+    using LY = NarrowLayout<NT>;
+    CUtensorMap tx, tw;
+    TRY(map_e4m3_sw128(&tx, x, p.M, p.K, NT));
+    TRY(map_e4m3_sw128(&tw, w, p.N, p.K, 128));
+    p.tiles_n = int(blocks128(p.N));
+    const long long tiles = (p.M + NT - 1) / NT * p.tiles_n;
+    if (tiles > INT_MAX / 8) return fail(PARARNN_ERR_INVALID_ARG, "too many tiles");
+    p.n_tiles = int(tiles);
+    // as many CTAs as there are SMs, twice over where two fit
+    const int room = sms * (LY::smem_bytes * 2 <= 227 * 1024 ? 2 : 1);
+    p.splits = 1;
+    while (p.splits < 8 && p.splits * 2 <= p.KB && tiles * p.splits * 2 <= room) p.splits *= 2;
+    void* args[] = {(void*)&tx, (void*)&tw, (void*)&p};
+    return launch_clusters(fp8_project_narrow_kernel<NT>, p.n_tiles * p.splits, kNThreads, p.splits, LY::smem_bytes, st, args);
+}
+
+template <int CG>
+pararnn_status launch_wide(const uint8_t* x, const uint8_t* w, Fp8Params p, int sms, cudaStream_t st)
+{
+    using LY = WideLayout<CG>;
+    CUtensorMap tx, tw, tu;
+    TRY(map_e4m3_sw128(&tx, x, p.M, p.K, kQM));
+    TRY(map_e4m3_sw128(&tw, w, p.N, p.K, kQN / CG));
+    TRY(map_sums_sw128(&tu, p.u, p.M, p.N, p.u_bf16));
+    p.tiles_n = int((p.N + kQN - 1) / kQN);
+    const long long tiles = (p.M + CG * kQM - 1) / (CG * kQM) * p.tiles_n;
+    if (tiles > INT_MAX / 8) return fail(PARARNN_ERR_INVALID_ARG, "too many tiles");
+    p.n_tiles = int(tiles);
+    p.splits = 1;
+    void* args[] = {(void*)&tx, (void*)&tw, (void*)&tu, (void*)&p};
+    return launch_clusters(fp8_project_wide_kernel<CG>, CG * std::min(p.n_tiles, sms / CG), kQThreads, CG, LY::smem_bytes, st, args);
+}
+
 }  // namespace
 
 extern "C" {
@@ -397,9 +488,14 @@ pararnn_status pararnn_fp8_quantize(const void* x, pararnn_dtype x_dtype, int bl
     return launched();
 }
 
+size_t pararnn_fp8_project_workspace_size(int64_t M, int64_t N, int64_t K)
+{
+    return fp8_dims(M, N, K) == PARARNN_OK ? sizeof(WsHeader) : 0;
+}
+
 pararnn_status pararnn_fp8_project(const void* x, const float* x_scale, const void* w, const float* w_scale,
                                    const float* bias, void* u, pararnn_dtype u_dtype, int64_t M, int64_t N, int64_t K,
-                                   pararnn_stream_t stream)
+                                   void* workspace, size_t workspace_bytes, pararnn_stream_t stream)
 {
     t_err[0] = '\0';
     TRY(check_wide_dtype(u_dtype, "u_dtype"));
@@ -412,11 +508,12 @@ pararnn_status pararnn_fp8_project(const void* x, const float* x_scale, const vo
     TRY(fp8_dims(M, N, K));
     const long long KB = blocks128(K);
     TRY((check_apart<5, 1>({{"x", x, size_t(M) * K}, {"x_scale", x_scale, size_t(M) * KB * 4}, {"w", w, size_t(N) * K},
-                           {"w_scale", w_scale, size_t(blocks128(N)) * KB * 4}, {"bias", bias, size_t(N) * 4}},
-                          {{"u", u, size_t(M) * N * dtype_bytes(u_dtype)}}, nullptr)));
+                            {"w_scale", w_scale, size_t(blocks128(N)) * KB * 4}, {"bias", bias, size_t(N) * 4}},
+                           {{"u", u, size_t(M) * N * dtype_bytes(u_dtype)}}, nullptr)));
+    TRY(check_workspace(workspace, workspace_bytes, sizeof(WsHeader)));
+    int sms = 0;
+    TRY(device_info(&sms));
     Fp8Params p;
-    p.x = static_cast<const uint8_t*>(x);
-    p.w = static_cast<const uint8_t*>(w);
     p.xs = x_scale;
     p.ws = w_scale;
     p.bias = bias;
@@ -424,12 +521,17 @@ pararnn_status pararnn_fp8_project(const void* x, const float* x_scale, const vo
     p.M = M;
     p.N = N;
     p.K = K;
-    p.KB = KB;
+    p.KB = int(KB);
     p.u_bf16 = u_dtype == PARARNN_BF16;
-    if ((M + 63) / 64 > 65535) return fail(PARARNN_ERR_INVALID_ARG, "M too large");
-    fp8_project_kernel<<<dim3(unsigned((N + 63) / 64), unsigned((M + 63) / 64)), 256, 0,
-                         reinterpret_cast<cudaStream_t>(stream)>>>(p);
-    return launched();
+    p.hdr = static_cast<WsHeader*>(workspace);
+    p.wait_ns = kWaitLimitNs;
+    const uint8_t *xb = static_cast<const uint8_t*>(x), *wb = static_cast<const uint8_t*>(w);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+        if (M >= 256) return launch_wide<2>(xb, wb, p, sms, st);
+    if (M > 64) return launch_narrow<128>(xb, wb, p, sms, st);
+    if (M > 32) return launch_narrow<64>(xb, wb, p, sms, st);
+    if (M > 16) return launch_narrow<32>(xb, wb, p, sms, st);
+    return launch_narrow<16>(xb, wb, p, sms, st);
 }
 
 }  // extern "C"

@@ -177,20 +177,24 @@ def test_fp8_refusals(capi):
         assert q(**bad) == capi.ERR_INVALID_ARG, bad
     assert q(K=24) == capi.ERR_UNSUPPORTED
 
-    def p(x=A[0], xs=A[1], w=A[2], ws=A[3], b=None, u=A[4], ud=1, M=4, N=16, K=32):
-        return capi.lib.pararnn_fp8_project(x, xs, w, ws, b, u, ud, M, N, K, None)
+    def p(x=A[0], xs=A[1], w=A[2], ws=A[3], b=None, u=A[4], ud=1, M=4, N=16, K=32, work=256, wb=1 << 10):
+        return capi.lib.pararnn_fp8_project(x, xs, w, ws, b, u, ud, M, N, K, work, wb, None)
 
     for bad in (dict(x=None), dict(xs=None), dict(w=None), dict(ws=None), dict(u=None), dict(ud=2), dict(M=0), dict(N=0),
                 dict(K=-16), dict(b=A[5] + 4), dict(u=A[0]), dict(u=A[2] - 16), dict(M=1 << 31)):
         assert p(**bad) == capi.ERR_INVALID_ARG, bad
     assert p(K=24) == capi.ERR_UNSUPPORTED
     assert p(N=12) == capi.ERR_UNSUPPORTED
+    assert p(work=None) == capi.ERR_WORKSPACE
+    assert p(wb=255) == capi.ERR_WORKSPACE
 
 
 def test_workspace_sizes(capi):
     for f in (capi.pararnn_glr_workspace_size, capi.pararnn_glr_adjoint_workspace_size):
         assert f(100, 3, 64) > 0 and f(100, 3, 64) % 256 == 0
         assert f(0, 3, 64) == 0 and f(100, 0, 64) == 0 and f(100, 3, 60) == 0 and f(1 << 31, 1, 64) == 0
+    f = capi.pararnn_fp8_project_workspace_size
+    assert f(5, 16, 32) == 256 and f(0, 16, 32) == 0 and f(5, 12, 32) == 0 and f(5, 16, 24) == 0
     f = capi.pararnn_rms_norm_adjoint_workspace_size
     assert f(100, 64) > 0 and f(100, 64) % 256 == 0
     assert f(0, 64) == 0 and f(100, 60) == 0 and f(100, 16392) == 0
@@ -203,7 +207,7 @@ def test_no_device_is_reported(capi):
     assert lib.pararnn_glr_scan(A[0], 1, A[1], None, None, A[9], None, 8, 2, 16, 256, 1 << 20, None) == capi.ERR_CUDA
     assert lib.pararnn_glr_step(A[0], 1, A[1], A[2], A[2], 2, 16, None) == capi.ERR_CUDA  # in place
     assert lib.pararnn_rms_norm(A[0], 1, A[1], 1, A[2], 1e-6, A[1], A[4], 1, None, None, 4, 32, None) == capi.ERR_CUDA
-    assert lib.pararnn_fp8_project(A[0], A[1], A[2], A[3], None, A[4], 1, 4, 16, 32, None) == capi.ERR_CUDA
+    assert lib.pararnn_fp8_project(A[0], A[1], A[2], A[3], None, A[4], 1, 4, 16, 32, 256, 256, None) == capi.ERR_CUDA
 
 
 # ----------------------------------------------------- the binding's refusals
