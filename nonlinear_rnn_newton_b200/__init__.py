@@ -71,5 +71,7 @@ __all__ = [
 def __getattr__(name):
     if name in __all__ or name == "capi":
         capi = importlib.import_module(".capi", __name__)
-        return capi if name == "capi" else getattr(capi, name)
+        value = capi if name == "capi" else getattr(capi, name)
+        globals()[name] = value  # the next use finds it without coming here
+        return value
     raise AttributeError(name)

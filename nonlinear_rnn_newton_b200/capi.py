@@ -710,30 +710,51 @@ def pararnn_selftest_wait_timeout(which, limit_ns, workspace, stream=None):
 
 
 # ------------------------------------------- layer operators (see pararnn.h)
+#
+# A decode step's kernels take a few microseconds, so the checks here are kept
+# to plain comparisons; _need is called to say what is wrong.
 
 _CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
+_WIDE = (torch.float32, torch.bfloat16)
+_f32, _e4m3 = torch.float32, torch.float8_e4m3fn
 
 
-def _code(t, name, allowed):
-    dtype = t if isinstance(t, torch.dtype) else t.dtype
+def _fits(t, name, shape, dtype, device):
+    """_need, quickly; t may not be None."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _need(t, name, shape, dtype, device)
+
+
+def _code(dtype, name, allowed):
     if dtype not in allowed:
         raise TypeError(f"{name} must be one of {', '.join(str(d) for d in allowed)}, got {dtype}")
     return _CODES[dtype]
 
 
-_WIDE = (torch.float32, torch.bfloat16)
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 def _run(fn, dev, stream, *args):
     """Call fn(*args, stream) with `dev` current; raises unless it returns OK."""
     if dev.type != "cuda":
         raise ValueError(f"device tensors are needed, got one on {dev}")
+    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            st = fn(*args, _stream(dev, stream))
+            st = fn(*args, raw)
     else:
-        st = fn(*args, _stream(dev, stream))
-    _check(st, allow=(OK,))
+        st = fn(*args, raw)
+    if st != OK:
+        _check(st, allow=(OK,))
+
+
+def _space(nbytes, dev, workspace):
+    """(address, bytes) of the caller's workspace, or of a new one (kept by the
+    stream's order until the call's work is done); and the tensor."""
+    if workspace is None:
+        workspace = torch.empty(nbytes or 256, dtype=torch.uint8, device=dev)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def pararnn_glr_workspace_size(T, n_seq, D):
@@ -747,27 +768,25 @@ def pararnn_glr_adjoint_workspace_size(T, n_seq, D):
 def _glr_args(u, rate, h0, seq_starts):
     """(rows' shape, T, n_seq, D) of a call on u [B,L,3,D], or on packed rows
     u [T,3,D] with seq_starts [n_seq + 1]."""
-    if u.dim() != (4 if seq_starts is None else 3) or u.shape[-2] != 3:
+    shape = u.shape
+    if len(shape) != (4 if seq_starts is None else 3) or shape[-2] != 3:
         raise ValueError("u must be [B,L,3,D], or [T,3,D] with seq_starts; got shape "
-                         f"{tuple(u.shape)} {'with' if seq_starts is not None else 'without'} seq_starts")
-    _code(u, "u", _WIDE)
+                         f"{tuple(shape)} {'with' if seq_starts is not None else 'without'} seq_starts")
+    _code(u.dtype, "u", _WIDE)
     if not u.is_contiguous():
         raise ValueError("u must be contiguous")
-    D = u.shape[-1]
+    D, dev = shape[-1], u.device
     if seq_starts is None:
-        n_seq, T = u.shape[0], u.shape[0] * u.shape[1]
+        n_seq, T = shape[0], shape[0] * shape[1]
     else:
         if seq_starts.dim() != 1 or seq_starts.numel() < 2:
             raise ValueError("seq_starts must be [n_seq + 1]")
-        n_seq, T = seq_starts.numel() - 1, u.shape[0]
-        _need(seq_starts, "seq_starts", (n_seq + 1,), dtype=torch.int32, device=u.device)
-    _need(rate, "rate", (D,), device=u.device)
-    _need(h0, "h0", (n_seq, D), device=u.device)
-    return tuple(u.shape[:-2]) + (D,), T, n_seq, D
-
-
-def _ws_args(ws):
-    return _ptr(ws), ws.numel() * ws.element_size()
+        n_seq, T = seq_starts.numel() - 1, shape[0]
+        _fits(seq_starts, "seq_starts", (n_seq + 1,), torch.int32, dev)
+    _fits(rate, "rate", (D,), _f32, dev)
+    if h0 is not None:
+        _fits(h0, "h0", (n_seq, D), _f32, dev)
+    return shape[:-2] + (D,), T, n_seq, D
 
 
 def pararnn_glr_scan(u, rate, h0=None, seq_starts=None, h=None, h_last=None, want_last=True, workspace=None,
@@ -780,14 +799,16 @@ def pararnn_glr_scan(u, rate, h0=None, seq_starts=None, h=None, h_last=None, wan
     shape, T, n_seq, D = _glr_args(u, rate, h0, seq_starts)
     dev = u.device
     if h is None:
-        h = torch.empty(shape, dtype=torch.float32, device=dev)
-    if h_last is None and want_last:
-        h_last = torch.empty((n_seq, D), dtype=torch.float32, device=dev)
-    _need(h, "h", shape, device=dev)
-    _need(h_last, "h_last", (n_seq, D), device=dev)
-    ws = _workspace(lib.pararnn_glr_workspace_size(T, n_seq, D), dev, workspace)
-    _run(lib.pararnn_glr_scan, dev, stream, _ptr(u), _dtype_code(u), _ptr(rate), _ptr(h0), _ptr(seq_starts), _ptr(h),
-         _ptr(h_last), T, n_seq, D, *_ws_args(ws))
+        h = torch.empty(shape, dtype=_f32, device=dev)
+    else:
+        _fits(h, "h", shape, _f32, dev)
+    if h_last is not None:
+        _fits(h_last, "h_last", (n_seq, D), _f32, dev)
+    elif want_last:
+        h_last = torch.empty((n_seq, D), dtype=_f32, device=dev)
+    ws, at, size = _space(lib.pararnn_glr_workspace_size(T, n_seq, D), dev, workspace)
+    _run(lib.pararnn_glr_scan, dev, stream, u.data_ptr(), _CODES[u.dtype], rate.data_ptr(), _address(h0),
+         _address(seq_starts), h.data_ptr(), _address(h_last), T, n_seq, D, at, size)
     return h, h_last
 
 
@@ -798,18 +819,26 @@ def pararnn_glr_adjoint(u, rate, h0, h, dh, dh_last=None, seq_starts=None, du=No
     Asynchronous on the stream."""
     shape, T, n_seq, D = _glr_args(u, rate, h0, seq_starts)
     dev = u.device
+    _fits(h, "h", shape, _f32, dev)
+    _fits(dh, "dh", shape, _f32, dev)
+    if dh_last is not None:
+        _fits(dh_last, "dh_last", (n_seq, D), _f32, dev)
     if du is None:
-        du = torch.empty(u.shape, dtype=torch.float32, device=dev)
+        du = torch.empty(u.shape, dtype=_f32, device=dev)
+    else:
+        _fits(du, "du", u.shape, _f32, dev)
     if drate is None:
-        drate = torch.empty((D,), dtype=torch.float32, device=dev)
-    if dh0 is None and want_dh0:
-        dh0 = torch.empty((n_seq, D), dtype=torch.float32, device=dev)
-    for t, n, s in ((h, "h", shape), (dh, "dh", shape), (dh_last, "dh_last", (n_seq, D)), (du, "du", u.shape),
-                    (drate, "drate", (D,)), (dh0, "dh0", (n_seq, D))):
-        _need(t, n, s, device=dev)
-    ws = _workspace(lib.pararnn_glr_adjoint_workspace_size(T, n_seq, D), dev, workspace)
-    _run(lib.pararnn_glr_adjoint, dev, stream, _ptr(u), _dtype_code(u), _ptr(rate), _ptr(h0), _ptr(seq_starts),
-         _ptr(h), _ptr(dh), _ptr(dh_last), _ptr(du), _ptr(drate), _ptr(dh0), T, n_seq, D, *_ws_args(ws))
+        drate = torch.empty((D,), dtype=_f32, device=dev)
+    else:
+        _fits(drate, "drate", (D,), _f32, dev)
+    if dh0 is not None:
+        _fits(dh0, "dh0", (n_seq, D), _f32, dev)
+    elif want_dh0:
+        dh0 = torch.empty((n_seq, D), dtype=_f32, device=dev)
+    ws, at, size = _space(lib.pararnn_glr_adjoint_workspace_size(T, n_seq, D), dev, workspace)
+    _run(lib.pararnn_glr_adjoint, dev, stream, u.data_ptr(), _CODES[u.dtype], rate.data_ptr(), _address(h0),
+         _address(seq_starts), h.data_ptr(), dh.data_ptr(), _address(dh_last), du.data_ptr(), drate.data_ptr(),
+         _address(dh0), T, n_seq, D, at, size)
     return du, drate, dh0
 
 
@@ -819,20 +848,27 @@ def pararnn_glr_step(u, rate, h_prev=None, h_next=None, stream=None):
     if u.dim() != 3 or u.shape[1] != 3:
         raise ValueError(f"u must be [B,3,D], got shape {tuple(u.shape)}")
     B, _, D = u.shape
-    _need(u, "u", (B, 3, D), dtype=u.dtype)
-    _need(rate, "rate", (D,), device=u.device)
-    _need(h_prev, "h_prev", (B, D), device=u.device)
+    dev = u.device
+    code = _code(u.dtype, "u", _WIDE)
+    if not u.is_contiguous():
+        raise ValueError("u must be contiguous")
+    _fits(rate, "rate", (D,), _f32, dev)
+    if h_prev is not None:
+        _fits(h_prev, "h_prev", (B, D), _f32, dev)
     if h_next is None:
-        h_next = torch.empty((B, D), dtype=torch.float32, device=u.device)
-    _need(h_next, "h_next", (B, D), device=u.device)
-    _run(lib.pararnn_glr_step, u.device, stream, _ptr(u), _dtype_code(u), _ptr(rate), _ptr(h_prev), _ptr(h_next), B, D)
+        h_next = torch.empty((B, D), dtype=_f32, device=dev)
+    else:
+        _fits(h_next, "h_next", (B, D), _f32, dev)
+    _run(lib.pararnn_glr_step, dev, stream, u.data_ptr(), code, rate.data_ptr(), _address(h_prev), h_next.data_ptr(), B,
+         D)
     return h_next
 
 
 def _rows(t, name):
     if t.dim() < 2:
         raise ValueError(f"{name} must have at least two dimensions")
-    return t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1]
+    D = t.shape[-1]
+    return t.numel() // D if D else 0, D
 
 
 def pararnn_rms_norm(x, w, residual=None, eps=1e-6, out_dtype=torch.bfloat16, sum=None, y=None, y_scale=None,
@@ -843,36 +879,40 @@ def pararnn_rms_norm(x, w, residual=None, eps=1e-6, out_dtype=torch.bfloat16, su
     the residual's type (None without a residual), rstd [...]).  sum may be
     the residual itself (in place)."""
     T, D = _rows(x, "x")
-    dev, shape = x.device, tuple(x.shape)
-    yc = _code(out_dtype, "out_dtype", tuple(_CODES))
-    _code(x, "x", _WIDE)
-    _need(x, "x", shape, dtype=x.dtype)
-    _need(w, "w", (D,), device=dev)
+    dev, shape = x.device, x.shape
+    yc = _code(out_dtype, "out_dtype", _CODES)
+    xc = _code(x.dtype, "x", _WIDE)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    _fits(w, "w", (D,), _f32, dev)
+    rc = F32
     if residual is not None:
-        rc = _code(residual, "residual", _WIDE)
-        _need(residual, "residual", shape, dtype=residual.dtype, device=dev)
+        rc = _code(residual.dtype, "residual", _WIDE)
+        _fits(residual, "residual", shape, residual.dtype, dev)
         if sum is None:
-            sum = torch.empty_like(residual)
-        _need(sum, "sum", shape, dtype=residual.dtype, device=dev)
-    else:
-        if sum is not None:
-            raise ValueError("sum is an output of a call with a residual")
-        rc = F32
+            sum = torch.empty(shape, dtype=residual.dtype, device=dev)
+        else:
+            _fits(sum, "sum", shape, residual.dtype, dev)
+    elif sum is not None:
+        raise ValueError("sum is an output of a call with a residual")
     if y is None:
         y = torch.empty(shape, dtype=out_dtype, device=dev)
-    _need(y, "y", shape, dtype=out_dtype, device=dev)
+    else:
+        _fits(y, "y", shape, out_dtype, dev)
     if yc == E4M3:
         blocks = shape[:-1] + ((D + 127) // 128,)
         if y_scale is None:
-            y_scale = torch.empty(blocks, dtype=torch.float32, device=dev)
-        _need(y_scale, "y_scale", blocks, device=dev)
+            y_scale = torch.empty(blocks, dtype=_f32, device=dev)
+        else:
+            _fits(y_scale, "y_scale", blocks, _f32, dev)
     elif y_scale is not None:
         raise ValueError("y_scale is an output of an 8-bit call")
     if rstd is None:
-        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    _need(rstd, "rstd", shape[:-1], device=dev)
-    _run(lib.pararnn_rms_norm, dev, stream, _ptr(x), _CODES[x.dtype], _ptr(residual), rc, _ptr(w), float(eps),
-         _ptr(sum), _ptr(y), yc, _ptr(y_scale), _ptr(rstd), T, D)
+        rstd = torch.empty(shape[:-1], dtype=_f32, device=dev)
+    else:
+        _fits(rstd, "rstd", shape[:-1], _f32, dev)
+    _run(lib.pararnn_rms_norm, dev, stream, x.data_ptr(), xc, _address(residual), rc, w.data_ptr(), eps, _address(sum),
+         y.data_ptr(), yc, _address(y_scale), rstd.data_ptr(), T, D)
     return y, y_scale, sum, rstd
 
 
@@ -887,22 +927,26 @@ def pararnn_rms_norm_adjoint(dy, sum, w, rstd, dsum=None, dx=None, dw=None, work
     sum's type, the gradient of x and residual alike, dw [D] fp32).  dx may be
     dsum itself."""
     T, D = _rows(sum, "sum")
-    dev, shape = sum.device, tuple(sum.shape)
-    sc, yc = _code(sum, "sum", _WIDE), _code(dy, "dy", _WIDE)
-    _need(sum, "sum", shape, dtype=sum.dtype)
-    _need(dy, "dy", shape, dtype=dy.dtype, device=dev)
-    _need(w, "w", (D,), device=dev)
-    _need(rstd, "rstd", shape[:-1], device=dev)
-    _need(dsum, "dsum", shape, dtype=sum.dtype, device=dev)
+    dev, shape = sum.device, sum.shape
+    sc, yc = _code(sum.dtype, "sum", _WIDE), _code(dy.dtype, "dy", _WIDE)
+    if not sum.is_contiguous():
+        raise ValueError("sum must be contiguous")
+    _fits(dy, "dy", shape, dy.dtype, dev)
+    _fits(w, "w", (D,), _f32, dev)
+    _fits(rstd, "rstd", shape[:-1], _f32, dev)
+    if dsum is not None:
+        _fits(dsum, "dsum", shape, sum.dtype, dev)
     if dx is None:
-        dx = torch.empty_like(sum)
+        dx = torch.empty(shape, dtype=sum.dtype, device=dev)
+    else:
+        _fits(dx, "dx", shape, sum.dtype, dev)
     if dw is None:
-        dw = torch.empty((D,), dtype=torch.float32, device=dev)
-    _need(dx, "dx", shape, dtype=sum.dtype, device=dev)
-    _need(dw, "dw", (D,), device=dev)
-    ws = _workspace(lib.pararnn_rms_norm_adjoint_workspace_size(T, D), dev, workspace)
-    _run(lib.pararnn_rms_norm_adjoint, dev, stream, _ptr(dy), yc, _ptr(sum), sc, _ptr(w), _ptr(rstd), _ptr(dsum),
-         _ptr(dx), _ptr(dw), T, D, *_ws_args(ws))
+        dw = torch.empty((D,), dtype=_f32, device=dev)
+    else:
+        _fits(dw, "dw", (D,), _f32, dev)
+    ws, at, size = _space(lib.pararnn_rms_norm_adjoint_workspace_size(T, D), dev, workspace)
+    _run(lib.pararnn_rms_norm_adjoint, dev, stream, dy.data_ptr(), yc, sum.data_ptr(), sc, w.data_ptr(),
+         rstd.data_ptr(), _address(dsum), dx.data_ptr(), dw.data_ptr(), T, D, at, size)
     return dx, dw
 
 
@@ -911,9 +955,10 @@ def pararnn_fp8_quantize(x, block_rows=1, q=None, scale=None, stream=None):
     columns (block_rows = 1, scale [..., ceil(K/128)]) or per 128 rows and 128
     columns (block_rows = 128, x [N,K], scale [ceil(N/128), ceil(K/128)])."""
     M, K = _rows(x, "x")
-    dev, shape = x.device, tuple(x.shape)
-    xc = _code(x, "x", _WIDE)
-    _need(x, "x", shape, dtype=x.dtype)
+    dev, shape = x.device, x.shape
+    xc = _code(x.dtype, "x", _WIDE)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     if block_rows == 1:
         blocks = shape[:-1] + ((K + 127) // 128,)
     elif block_rows == 128:
@@ -923,12 +968,14 @@ def pararnn_fp8_quantize(x, block_rows=1, q=None, scale=None, stream=None):
     else:
         raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
     if q is None:
-        q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+        q = torch.empty(shape, dtype=_e4m3, device=dev)
+    else:
+        _fits(q, "q", shape, _e4m3, dev)
     if scale is None:
-        scale = torch.empty(blocks, dtype=torch.float32, device=dev)
-    _need(q, "q", shape, dtype=torch.float8_e4m3fn, device=dev)
-    _need(scale, "scale", blocks, device=dev)
-    _run(lib.pararnn_fp8_quantize, dev, stream, _ptr(x), xc, block_rows, _ptr(q), _ptr(scale), M, K)
+        scale = torch.empty(blocks, dtype=_f32, device=dev)
+    else:
+        _fits(scale, "scale", blocks, _f32, dev)
+    _run(lib.pararnn_fp8_quantize, dev, stream, x.data_ptr(), xc, block_rows, q.data_ptr(), scale.data_ptr(), M, K)
     return q, scale
 
 
@@ -942,20 +989,22 @@ def pararnn_fp8_project(x, x_scale, w, w_scale, bias=None, out_dtype=torch.bfloa
     their scales (pararnn_rms_norm or pararnn_fp8_quantize), bias [N] fp32 or
     None.  Returns u [..., N] in out_dtype (bf16 or fp32)."""
     M, K = _rows(x, "x")
-    dev, shape = x.device, tuple(x.shape)
+    dev, shape = x.device, x.shape
     if w.dim() != 2 or w.shape[1] != K:
         raise ValueError(f"w must be [N,{K}], got {tuple(w.shape)}")
-    N = w.shape[0]
+    N, KB = w.shape[0], (K + 127) // 128
     uc = _code(out_dtype, "out_dtype", _WIDE)
-    _need(x, "x", shape, dtype=torch.float8_e4m3fn)
-    _need(x_scale, "x_scale", shape[:-1] + ((K + 127) // 128,), device=dev)
-    _need(w, "w", (N, K), dtype=torch.float8_e4m3fn, device=dev)
-    _need(w_scale, "w_scale", ((N + 127) // 128, (K + 127) // 128), device=dev)
-    _need(bias, "bias", (N,), device=dev)
+    _fits(x, "x", shape, _e4m3, dev)
+    _fits(x_scale, "x_scale", shape[:-1] + (KB,), _f32, dev)
+    _fits(w, "w", (N, K), _e4m3, dev)
+    _fits(w_scale, "w_scale", ((N + 127) // 128, KB), _f32, dev)
+    if bias is not None:
+        _fits(bias, "bias", (N,), _f32, dev)
     if u is None:
         u = torch.empty(shape[:-1] + (N,), dtype=out_dtype, device=dev)
-    _need(u, "u", shape[:-1] + (N,), dtype=out_dtype, device=dev)
-    ws = _workspace(lib.pararnn_fp8_project_workspace_size(M, N, K), dev, workspace)
-    _run(lib.pararnn_fp8_project, dev, stream, _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(u), uc,
-         M, N, K, *_ws_args(ws))
+    else:
+        _fits(u, "u", shape[:-1] + (N,), out_dtype, dev)
+    ws, at, size = _space(lib.pararnn_fp8_project_workspace_size(M, N, K), dev, workspace)
+    _run(lib.pararnn_fp8_project, dev, stream, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+         _address(bias), u.data_ptr(), uc, M, N, K, at, size)
     return u

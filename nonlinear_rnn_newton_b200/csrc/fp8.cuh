@@ -71,11 +71,9 @@ __device__ __forceinline__ void umma_e4m3(uint32_t tmem_d, uint64_t adesc, uint6
 
 // arrive on the barrier at this offset in both CTAs of the pair once every
 // product issued so far is done
-template <int CG>
-__device__ __forceinline__ void umma_commit_cg(uint64_t* bar)
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar)
 {
-    if constexpr (CG == 1) umma_commit(bar);
-    else asm volatile(
+    asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_addr(bar)),
         "h"(uint16_t(3))
@@ -141,16 +139,9 @@ __device__ __forceinline__ bool mbar_wait_clocked(uint64_t* bar, uint32_t parity
 
 // A tiled load into this CTA's shared memory that completes on a barrier of
 // either CTA of the pair (no multicast).
-template <int CG>
-__device__ __forceinline__ void tma_load_2d_cg(void* dst, const CUtensorMap* tm, int c0, int c1, uint32_t bar)
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* tm, int c0, int c1, uint32_t bar)
 {
-    if constexpr (CG == 1)
-        asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
-        "l"(tm), "r"(c0), "r"(c1), "r"(bar)
-        : "memory");
-    else asm volatile(
+    asm volatile(
         "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
         "l"(tm), "r"(c0), "r"(c1), "r"(bar)
@@ -245,15 +236,12 @@ constexpr int kQM = 128;       // rows of x a CTA (256 a pair)
 constexpr int kQN = 256;       // columns of a pair's tile
 constexpr int kQThreads = 384;
 constexpr int kQAhead = 4;     // blocks that a thread fetches its scales ahead
-template <int CG>
-struct WideLayout {
-    static constexpr int kStages = CG == 2 ? 6 : 4;
-    static constexpr size_t stage_bytes = size_t(kQM + kQN / CG) * kQK;
-    static constexpr size_t off_out = kStages * stage_bytes;  // 4 KB a reading warp
-    static constexpr size_t off_bar = off_out + 8 * 4096;
-    static constexpr size_t smem_bytes = off_bar + (2 * kStages + 4) * 8 + 16 + 1024;
-    static_assert(smem_bytes <= 232448, "shared memory");
-};
+constexpr int kQStages = 5;
+constexpr size_t kQStageBytes = size_t(kQM + kQN / 2) * kQK;
+constexpr size_t kQOut = kQStages * kQStageBytes;  // 2 x 4 KB a reading warp
+constexpr size_t kQBar = kQOut + 8 * 8192;
+constexpr size_t kQSmem = kQBar + (2 * kQStages + 4) * 8 + 16 + 1024;
+static_assert(kQSmem <= 232448, "shared memory");
 
 // Stores a tile of this CTA's shared memory (written by the generic proxy,
 // fenced) to a tensor; rows and columns beyond it are clipped.
@@ -265,61 +253,62 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, const void* 
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// the stores issued so far have read their shared memory
-__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+// all but the last `Left` stores issued have read their shared memory
+template <int Left>
+__device__ __forceinline__ void tma_store_wait_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(Left) : "memory");
+}
 
 // A warp's 32 rows x 128 columns of sums, a row a thread, to rows m0 and
 // columns n0 of u: by pieces of 128 bytes a row through 4 KB of shared memory
-// in the 128-byte swizzle (16-byte piece i of row r at i ^ (r % 8): eight
-// rows' writes fall in distinct banks) and a bulk store of the piece.  Writing
-// the rows from registers, 16 bytes a row and instruction, took 250 of 650 us
-// at M 32768, N 6144, K 2048.
+// (two in turn) in the 128-byte swizzle (16-byte piece i of row r at i ^ (r %
+// 8): eight rows' writes fall in distinct banks) and a bulk store of the
+// piece.  Writing the rows from registers, 16 bytes a row and instruction,
+// took 250 of 650 us at M 32768, N 6144, K 2048.  Lane l holds the bias of
+// columns 4 l .. 4 l + 3.
 template <bool Bf16>
 __device__ __forceinline__ void store_sums(const Fp8Params& p, const CUtensorMap* tm_u, unsigned char* stage, int m0,
-                                           int n0, int lane, const float (&acc)[128])
+                                           int n0, int lane, float4 bias, float (&acc)[128])
 {
     constexpr int kCols = Bf16 ? 64 : 32;  // columns of a piece
+    constexpr int kPer = kCols / 8;        // columns of 16 bytes
+    if (p.bias) {
+#pragma unroll
+        for (int j = 0; j < 128; j += 4) {
+            acc[j] += __shfl_sync(0xffffffffu, bias.x, j / 4);
+            acc[j + 1] += __shfl_sync(0xffffffffu, bias.y, j / 4);
+            acc[j + 2] += __shfl_sync(0xffffffffu, bias.z, j / 4);
+            acc[j + 3] += __shfl_sync(0xffffffffu, bias.w, j / 4);
+        }
+    }
 #pragma unroll
     for (int c = 0; c < 128; c += kCols) {
         if (n0 + c >= p.N) break;
-        if (lane == 0) tma_store_wait_read();  // the piece before has left
+        unsigned char* buf = stage + (c / kCols & 1) * 4096;
+        if (lane == 0) tma_store_wait_read<1>();  // the piece before the last has left
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            constexpr int kPer = kCols / 8;  // columns of 16 bytes
-            float v[kPer];
-#pragma unroll
-            for (int k = 0; k < kPer; k += 4) {
-                float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-                const int n = n0 + c + i * kPer + k;
-                if (p.bias && n < p.N) b = __ldg(reinterpret_cast<const float4*>(p.bias + n));
-                v[k] = acc[c + i * kPer + k] + b.x;
-                v[k + 1] = acc[c + i * kPer + k + 1] + b.y;
-                v[k + 2] = acc[c + i * kPer + k + 2] + b.z;
-                v[k + 3] = acc[c + i * kPer + k + 3] + b.w;
-            }
+            const float* v = acc + c + i * kPer;
             uint4 o;
             if constexpr (Bf16)
                 o = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                                pack_bf16x2(v[6], v[7]));
             else
                 o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) = o;
+            *reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) = o;
         }
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) tma_store_2d(tm_u, stage, n0 + c, m0);
+        if (lane == 0) tma_store_2d(tm_u, buf, n0 + c, m0);
     }
 }
 
-template <int CG>
-__global__ void __launch_bounds__(kQThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
     fp8_project_wide_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                             const __grid_constant__ CUtensorMap tm_u, const Fp8Params p)
 {
-    using LY = WideLayout<CG>;
-    constexpr int kQStages = LY::kStages;
-    constexpr size_t kQStageBytes = LY::stage_bytes, kQBar = LY::off_bar;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kQBar);  // the leading CTA's: both CTAs' loads
@@ -329,8 +318,8 @@ __global__ void __launch_bounds__(kQThreads, 1)
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(tempty + 2);
 
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-    const int pair = blockIdx.x / CG, pairs = gridDim.x / CG;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     int* err = &p.hdr->error;
     bool ok = true;
 
@@ -342,16 +331,16 @@ __global__ void __launch_bounds__(kQThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], CG * 8);
+            mbar_init(&tempty[i], 2 * 8);
         }
         fence_mbar_init();
         prefetch_tensormap(&tm_x);
         prefetch_tensormap(&tm_w);
     }
-    if (w == 0) tmem_alloc_cg<CG>(s_tmem, 512);
+    if (w == 0) tmem_alloc_cg<2>(s_tmem, 512);
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync_all();
+    cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
 
@@ -368,14 +357,14 @@ __global__ void __launch_bounds__(kQThreads, 1)
                         break;
                     }
                     unsigned char* sp = smem + s * kQStageBytes;
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], uint32_t(CG * kQStageBytes));
-                    const uint32_t bar = CG == 2 ? mapa(&full[s], 0) : smem_addr(&full[s]);
-                    tma_load_2d_cg<CG>(sp, &tm_x, kb * kQK, tm * CG * kQM + int(rank) * kQM, bar);
-                    tma_load_2d_cg<CG>(sp + kQM * kQK, &tm_w, kb * kQK, tn * kQN + int(rank) * (kQN / 2), bar);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], uint32_t(2 * kQStageBytes));
+                    const uint32_t bar = mapa(&full[s], 0);
+                    tma_load_2d_pair(sp, &tm_x, kb * kQK, tm * 2 * kQM + int(rank) * kQM, bar);
+                    tma_load_2d_pair(sp + kQM * kQK, &tm_w, kb * kQK, tn * kQN + int(rank) * (kQN / 2), bar);
                 }
             }
         } else if (w == 1 && lane == 0 && rank == 0) {
-            constexpr uint32_t kIdesc = idesc_e4m3(CG * kQM, kQN);
+            constexpr uint32_t kIdesc = idesc_e4m3(2 * kQM, kQN);
             int q = 0;
             for (int t = pair; t < p.n_tiles && ok; t += pairs) {
                 for (int kb = 0; kb < p.KB && ok; ++kb, ++q) {
@@ -391,9 +380,9 @@ __global__ void __launch_bounds__(kQThreads, 1)
                     const uint64_t ad = smem_desc_sw128(sp), bd = smem_desc_sw128(sp + kQM * kQK);
 #pragma unroll
                     for (int k = 0; k < kQK / 32; ++k)  // 32 bytes apart inside the swizzle atom
-                        umma_e4m3<CG>(tmem + uint32_t(b) * kQN, ad + uint64_t(2 * k), bd + uint64_t(2 * k), kIdesc, k != 0);
-                    umma_commit_cg<CG>(&empty[s]);
-                    umma_commit_cg<CG>(&tfull[b]);
+                        umma_e4m3<2>(tmem + uint32_t(b) * kQN, ad + uint64_t(2 * k), bd + uint64_t(2 * k), kIdesc, k != 0);
+                    umma_commit_pair(&empty[s]);
+                    umma_commit_pair(&tfull[b]);
                 }
             }
         }
@@ -402,15 +391,17 @@ __global__ void __launch_bounds__(kQThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int lq = w & 3, half = (w >> 2) - 1;
         const uint32_t ta = tmem + (uint32_t(32 * lq) << 16) + uint32_t(half) * 128;
-        unsigned char* out = smem + LY::off_out + (w - 4) * 4096;
+        unsigned char* out = smem + kQOut + (w - 4) * 8192;
         int q = 0;
         for (int t = pair; t < p.n_tiles && ok; t += pairs) {
             const int tm = t / p.tiles_n, tn = t - tm * p.tiles_n;
-            const long long m = (long long)tm * CG * kQM + rank * kQM + 32 * lq + lane;
+            const long long m = (long long)tm * 2 * kQM + rank * kQM + 32 * lq + lane;
             const long long n = (long long)tn * kQN + half * 128;
             const bool in = m < p.M && n < p.N;
             const float* xs = p.xs + m * p.KB;
             const float* ws = p.ws + n / 128 * p.KB;
+            float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p.bias && n + 4 * lane < p.N) bias = __ldg(reinterpret_cast<const float4*>(p.bias + n) + lane);
             float acc[128];
 #pragma unroll
             for (int j = 0; j < 128; ++j) acc[j] = 0.f;
@@ -445,10 +436,7 @@ __global__ void __launch_bounds__(kQThreads, 1)
                     } else {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) {
-                            if (CG == 2) mbar_arrive_cluster(mapa(&tempty[b], 0));
-                            else mbar_arrive(&tempty[b]);
-                        }
+                        if (lane == 0) mbar_arrive_cluster(mapa(&tempty[b], 0));
                     }
 #pragma unroll
                     for (int j = 0; j < 32; j += 2)
@@ -456,20 +444,20 @@ __global__ void __launch_bounds__(kQThreads, 1)
                 }
             }
             if (ok) {
-                const int m0 = tm * CG * kQM + int(rank) * kQM + 32 * lq;
+                const int m0 = tm * 2 * kQM + int(rank) * kQM + 32 * lq;
                 if (m0 < p.M && n < p.N) {
-                    if (p.u_bf16) store_sums<true>(p, &tm_u, out, m0, int(n), lane, acc);
-                    else store_sums<false>(p, &tm_u, out, m0, int(n), lane, acc);
+                    if (p.u_bf16) store_sums<true>(p, &tm_u, out, m0, int(n), lane, bias, acc);
+                    else store_sums<false>(p, &tm_u, out, m0, int(n), lane, bias, acc);
                 }
             }
         }
-        if (lane == 0) tma_store_wait_read();
+        if (lane == 0) tma_store_wait_read<0>();
     }
     if (!ok) let_copies_land();
     tc_fence_before();
     __syncthreads();
-    if (CG == 2) cluster_sync_all();
-    if (w == 0) tmem_dealloc_cg<CG>(tmem, 512);
+    cluster_sync_all();
+    if (w == 0) tmem_dealloc_cg<2>(tmem, 512);
 }
 
 // ---------------------------------------------------------------- narrow form

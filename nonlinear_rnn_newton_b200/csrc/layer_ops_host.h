@@ -255,21 +255,19 @@ pararnn_status launch_narrow(const uint8_t* x, const uint8_t* w, Fp8Params p, in
     return launch_clusters(fp8_project_narrow_kernel<NT>, p.n_tiles * p.splits, kNThreads, p.splits, LY::smem_bytes, st, args);
 }
 
-template <int CG>
 pararnn_status launch_wide(const uint8_t* x, const uint8_t* w, Fp8Params p, int sms, cudaStream_t st)
 {
-    using LY = WideLayout<CG>;
     CUtensorMap tx, tw, tu;
     TRY(map_e4m3_sw128(&tx, x, p.M, p.K, kQM));
-    TRY(map_e4m3_sw128(&tw, w, p.N, p.K, kQN / CG));
+    TRY(map_e4m3_sw128(&tw, w, p.N, p.K, kQN / 2));
     TRY(map_sums_sw128(&tu, p.u, p.M, p.N, p.u_bf16));
     p.tiles_n = int((p.N + kQN - 1) / kQN);
-    const long long tiles = (p.M + CG * kQM - 1) / (CG * kQM) * p.tiles_n;
+    const long long tiles = (p.M + 2 * kQM - 1) / (2 * kQM) * p.tiles_n;
     if (tiles > INT_MAX / 8) return fail(PARARNN_ERR_INVALID_ARG, "too many tiles");
     p.n_tiles = int(tiles);
     p.splits = 1;
     void* args[] = {(void*)&tx, (void*)&tw, (void*)&tu, (void*)&p};
-    return launch_clusters(fp8_project_wide_kernel<CG>, CG * std::min(p.n_tiles, sms / CG), kQThreads, CG, LY::smem_bytes, st, args);
+    return launch_clusters(fp8_project_wide_kernel, 2 * std::min(p.n_tiles, sms / 2), kQThreads, 2, kQSmem, st, args);
 }
 
 }  // namespace
@@ -527,7 +525,7 @@ pararnn_status pararnn_fp8_project(const void* x, const float* x_scale, const vo
     p.wait_ns = kWaitLimitNs;
     const uint8_t *xb = static_cast<const uint8_t*>(x), *wb = static_cast<const uint8_t*>(w);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-        if (M >= 256) return launch_wide<2>(xb, wb, p, sms, st);
+        if (M >= 256) return launch_wide(xb, wb, p, sms, st);
     if (M > 64) return launch_narrow<128>(xb, wb, p, sms, st);
     if (M > 32) return launch_narrow<64>(xb, wb, p, sms, st);
     if (M > 16) return launch_narrow<32>(xb, wb, p, sms, st);
