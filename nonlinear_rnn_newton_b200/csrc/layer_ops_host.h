@@ -82,32 +82,107 @@ pararnn_status check_starts(const void* starts)
     return PARARNN_OK;
 }
 
+// header | flags [tiles][S] | maps [tiles][S][32] (16 bytes each) | parts of
+// the rates' gradients [P][D]; the leading two are zeroed before each launch
+// where CTAs share a slab.
+struct GlrLayout {
+    size_t flags, maps, part, total;
+    int S, tiles;
+};
+
+GlrLayout glr_layout(long long T, long long D, int tile)
+{
+    GlrLayout ly;
+    ly.S = int((D + kGD - 1) / kGD);
+    ly.tiles = int((T + tile - 1) / tile);
+    ly.flags = sizeof(WsHeader);
+    ly.maps = align256(ly.flags + size_t(ly.tiles) * ly.S * 4);
+    ly.part = ly.maps + size_t(ly.tiles) * ly.S * 512;
+    ly.total = align256(ly.part + size_t(kGMaxP) * D * 4);
+    return ly;
+}
+
 size_t glr_ws_bytes(bool adjoint, long long T, long long n_seq, long long D)
 {
     if (T < 1 || n_seq < 1 || D < 1 || D % 8 != 0 || T > INT_MAX / 2 || n_seq > INT_MAX / 2 || D > INT_MAX / 2 ||
         (double)T * (double)D * 12.0 >= kMaxBytes || (double)n_seq * (double)D * 4.0 >= kMaxBytes)
         return 0;
-    return adjoint ? align256(size_t(n_seq) * D * 4) : 256;
+    // fp32 gates have the shorter tiles
+    return glr_layout(T, D, adjoint ? GlrAdjointLayout<float>::kTile : GlrScanLayout<float>::kTile).total;
+}
+
+// rows [T][width] (u: width 3 D, as [T][3][D]) -> box of `rows` rows of 64
+// channels (all three gates)
+pararnn_status map_glr(CUtensorMap* m, const void* x, pararnn_dtype dt, int gates, long long T, long long D, int rows)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return fail(PARARNN_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+    const cuuint64_t es = dtype_bytes(dt);
+    const bool u = gates > 1;
+    cuuint64_t dims[3] = {cuuint64_t(D), u ? cuuint64_t(gates) : cuuint64_t(T), cuuint64_t(T)};
+    cuuint64_t strides[2] = {cuuint64_t(D) * es, cuuint64_t(D) * es * gates};
+    cuuint32_t box[3] = {cuuint32_t(kGD), u ? cuuint32_t(gates) : cuuint32_t(rows), cuuint32_t(rows)};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    CUresult r = enc(m, dt == PARARNN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                     u ? 3 : 2, const_cast<void*>(x), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PARARNN_ERR_CUDA, "cuTensorMapEncodeTiled(recurrence) failed: %d", int(r));
+    return PARARNN_OK;
+}
+
+// How many CTAs share a slab: what fits on the device at once, at most one
+// CTA a tile and kGMaxP.  They wait for one another only if there are several.
+template <class K>
+pararnn_status launch_glr(K kern, int threads, size_t smem, const GlrLayout& ly, GlrParams* p, void** args, void* ws,
+                          cudaStream_t st)
+{
+    int sms = 0, occ = 0;
+    TRY(device_info(&sms));
+    const void* f = reinterpret_cast<const void*>(kern);
+    CUDA_TRY(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+    CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, threads, smem));
+    if (occ < 1) return fail(PARARNN_ERR_CUDA, "kernel does not fit on an SM (smem %zu)", smem);
+    unsigned char* base = static_cast<unsigned char*>(ws);
+    p->S = ly.S;
+    p->tiles = ly.tiles;
+    p->P = std::max(1, std::min({occ * sms / ly.S, ly.tiles, kGMaxP}));
+    p->hdr = reinterpret_cast<WsHeader*>(base);
+    p->flags = reinterpret_cast<unsigned*>(base + ly.flags);
+    p->maps = reinterpret_cast<float4*>(base + ly.maps);
+    p->part = reinterpret_cast<float*>(base + ly.part);
+    p->wait_ns = kWaitLimitNs;
+    const dim3 grid(unsigned(ly.S) * p->P);
+    if (p->P > 1) {
+        CUDA_TRY(cudaMemsetAsync(ws, 0, ly.maps, st));
+        CUDA_TRY(cudaLaunchCooperativeKernel(f, grid, dim3(threads), args, smem, st));
+    } else {
+        CUDA_TRY(cudaLaunchKernel(f, grid, dim3(threads), args, smem, st));
+    }
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    return PARARNN_OK;
 }
 
 template <class UT>
-pararnn_status launch_glr_scan(const UT* u, const float* rate, const float* h0, const int* starts, float* h,
-                               float* h_last, long long T, long long n_seq, long long D, cudaStream_t st)
+pararnn_status launch_glr_scan(const UT* u, GlrParams p, long long D, void* ws, cudaStream_t st)
 {
-    glr_scan_seq_kernel<UT><<<unsigned((n_seq * D + 63) / 64), 64, 0, st>>>(u, rate, h0, starts, h, h_last, T, n_seq, D);
-    return launched();
+    using LY = GlrScanLayout<UT>;
+    CUtensorMap tu;
+    TRY(map_glr(&tu, u, sizeof(UT) == 2 ? PARARNN_BF16 : PARARNN_F32, 3, p.T, D, LY::kTile));
+    void* args[] = {(void*)&tu, (void*)&p};
+    return launch_glr(glr_scan_kernel<UT>, kGThreads, LY::smem_bytes, glr_layout(p.T, D, LY::kTile), &p, args, ws, st);
 }
 
 template <class UT>
-pararnn_status launch_glr_adjoint(const UT* u, const float* rate, const float* h0, const int* starts, const float* h,
-                                  const float* dh, const float* dh_last, float* du, float* drate, float* dh0,
-                                  long long T, long long n_seq, long long D, void* ws, cudaStream_t st)
+pararnn_status launch_glr_adjoint(const UT* u, GlrParams p, float* drate, long long D, void* ws, cudaStream_t st)
 {
-    float* part = static_cast<float*>(ws);
-    glr_adjoint_seq_kernel<UT><<<unsigned((n_seq * D + 63) / 64), 64, 0, st>>>(u, rate, h0, starts, h, dh, dh_last, du,
-                                                                              dh0, part, T, n_seq, D);
-    TRY(launched());
-    column_sum_kernel<<<unsigned((D + 31) / 32), 256, 0, st>>>(part, drate, n_seq, D);
+    using LY = GlrAdjointLayout<UT>;
+    CUtensorMap tu, th, td;
+    TRY(map_glr(&tu, u, sizeof(UT) == 2 ? PARARNN_BF16 : PARARNN_F32, 3, p.T, D, LY::kTile));
+    TRY(map_glr(&th, p.states, PARARNN_F32, 1, p.T, D, LY::kTile));
+    TRY(map_glr(&td, p.dh, PARARNN_F32, 1, p.T, D, LY::kTile));
+    void* args[] = {(void*)&tu, (void*)&th, (void*)&td, (void*)&p};
+    TRY(launch_glr(glr_adjoint_kernel<UT>, kGThreads, LY::smem_bytes, glr_layout(p.T, D, LY::kTile), &p, args, ws, st));
+    column_sum_kernel<<<unsigned((D + 31) / 32), 256, 0, st>>>(p.part, drate, p.P, D);
     return launched();
 }
 
@@ -296,9 +371,18 @@ pararnn_status pararnn_glr_scan(const void* u, pararnn_dtype u_dtype, const floa
                           {{"h", h, rows * 4}, {"h_last", h_last, ends}}, nullptr)));
     TRY(check_workspace(workspace, workspace_bytes, glr_ws_bytes(false, T, n_seq, D)));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (u_dtype == PARARNN_BF16)
-        return launch_glr_scan(static_cast<const uint16_t*>(u), rate, h0, seq_starts, h, h_last, T, n_seq, D, st);
-    return launch_glr_scan(static_cast<const float*>(u), rate, h0, seq_starts, h, h_last, T, n_seq, D, st);
+    GlrParams p = {};
+    p.rate = rate;
+    p.h0 = h0;
+    p.starts = seq_starts;
+    p.h = h;
+    p.h_last = h_last;
+    p.D = D;
+    p.T = int(T);
+    p.n_seq = int(n_seq);
+    p.L = int(T / n_seq);
+    if (u_dtype == PARARNN_BF16) return launch_glr_scan(static_cast<const uint16_t*>(u), p, D, workspace, st);
+    return launch_glr_scan(static_cast<const float*>(u), p, D, workspace, st);
 }
 
 pararnn_status pararnn_glr_adjoint(const void* u, pararnn_dtype u_dtype, const float* rate, const float* h0,
@@ -326,11 +410,21 @@ pararnn_status pararnn_glr_adjoint(const void* u, pararnn_dtype u_dtype, const f
                           {{"du", du, rows * 12}, {"drate", drate, size_t(D) * 4}, {"dh0", dh0, ends}}, nullptr)));
     TRY(check_workspace(workspace, workspace_bytes, glr_ws_bytes(true, T, n_seq, D)));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (u_dtype == PARARNN_BF16)
-        return launch_glr_adjoint(static_cast<const uint16_t*>(u), rate, h0, seq_starts, h, dh, dh_last, du, drate, dh0,
-                                  T, n_seq, D, workspace, st);
-    return launch_glr_adjoint(static_cast<const float*>(u), rate, h0, seq_starts, h, dh, dh_last, du, drate, dh0, T,
-                              n_seq, D, workspace, st);
+    GlrParams p = {};
+    p.rate = rate;
+    p.h0 = h0;
+    p.starts = seq_starts;
+    p.states = h;
+    p.dh = dh;
+    p.dh_last = dh_last;
+    p.du = du;
+    p.dh0 = dh0;
+    p.D = D;
+    p.T = int(T);
+    p.n_seq = int(n_seq);
+    p.L = int(T / n_seq);
+    if (u_dtype == PARARNN_BF16) return launch_glr_adjoint(static_cast<const uint16_t*>(u), p, drate, D, workspace, st);
+    return launch_glr_adjoint(static_cast<const float*>(u), p, drate, D, workspace, st);
 }
 
 pararnn_status pararnn_glr_step(const void* u, pararnn_dtype u_dtype, const float* rate, const float* h_prev,
