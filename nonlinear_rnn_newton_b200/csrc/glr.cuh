@@ -14,48 +14,50 @@
 //   dr = dl l (1 - sig(r)),  ds = sum dl sig(r),  dh0 = G of the first row.
 #pragma once
 
+#include <type_traits>
+
 #include "fp8.cuh"  // bounded waits counted in clocks
 
 namespace pararnn {
 
 // ------------------------------------------------------------------ numerics
 
-// s(x) = 1 / (1 + e^-x) with its own reciprocal: e^-x = inf gives exactly 0,
-// so a gate at the type's lowest value (or -inf) is shut and not nearly shut.
-__device__ __forceinline__ float logistic(float x) { return rcp_approx(1.0f + ex2_approx(-kLog2e * x)); }
-
-// 1 - e^-l for l >= 0.  Below 1/4 from its series up to l^6 (the first term
+// s(x) = 1 / (1 + e^-x) takes a reciprocal of its own: e^-x = inf then gives
+// exactly 0, so a gate at the type's lowest value (or -inf) is shut and not
+// nearly shut.
+//
+// p = 1 - e^-l for l >= 0: below 1/4 from its series up to l^6 (the first term
 // left out is l^7/5040, 5e-8 of the value), since 1 - ex2.approx would keep
 // only the bits of e^-l below 1: at l = 1e-3, a common decay, four digits.
-__device__ __forceinline__ float one_minus_exp(float l)
+// Pairs of neighbouring channels: the packed fp32 instructions of this
+// architecture take both at once.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 neg(float2 x) { return make_float2(-x.x, -x.y); }
+
+// Near: every rate of the warp is below 1/4, so l <= rate is too and the far
+// branch (with its special-function use) is left out.
+template <bool Near>
+__device__ __forceinline__ float2 one_minus_exp(float2 l)
 {
-    float t = fmaf(l, -1.0f / 720, 1.0f / 120);
-    t = fmaf(l, t, -1.0f / 24);
-    t = fmaf(l, t, 1.0f / 6);
-    t = fmaf(l, t, -0.5f);
-    t = fmaf(l, t, 1.0f);
-    const float far = 1.0f - ex2_approx(-kLog2e * l);
-    return l < 0.25f ? l * t : far;
+    float2 t = __ffma2_rn(l, both(-1.0f / 720), both(1.0f / 120));
+    t = __ffma2_rn(l, t, both(-1.0f / 24));
+    t = __ffma2_rn(l, t, both(1.0f / 6));
+    t = __ffma2_rn(l, t, both(-0.5f));
+    t = __ffma2_rn(l, t, both(1.0f));
+    t = __fmul2_rn(l, t);
+    if constexpr (!Near) {
+        const float fx = 1.0f - ex2_approx(-kLog2e * l.x), fy = 1.0f - ex2_approx(-kLog2e * l.y);
+        t = make_float2(l.x < 0.25f ? t.x : fx, l.y < 0.25f ? t.y : fy);
+    }
+    return t;
 }
 
-struct GlrStep {
-    float sr, si, l, a, q;  // q = m^2
-};
-
-// from sr = s(r)
-__device__ __forceinline__ GlrStep glr_open(float sr, float i, float rate)
+__device__ __forceinline__ float2 logistic(float2 x)
 {
-    GlrStep g;
-    g.sr = sr;
-    g.si = logistic(i);
-    g.l = rate * g.sr;
-    const float p = one_minus_exp(g.l);
-    g.a = 1.0f - p;
-    g.q = p * (2.0f - p);
-    return g;
+    const float2 y = __fmul2_rn(x, both(-kLog2e));
+    const float2 d = __fadd2_rn(make_float2(ex2_approx(y.x), ex2_approx(y.y)), both(1.0f));
+    return make_float2(rcp_approx(d.x), rcp_approx(d.y));
 }
-
-__device__ __forceinline__ GlrStep glr_gates(float r, float i, float rate) { return glr_open(logistic(r), i, rate); }
 
 __device__ __forceinline__ float sqrt_approx(float x)
 {
@@ -69,6 +71,31 @@ __device__ __forceinline__ float rsqrt_approx(float x)
     float r;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// l = s sr, a = e^-l, q = 1 - a^2
+struct Decay2 {
+    float2 l, a, q;
+};
+
+template <bool Near>
+__device__ __forceinline__ Decay2 glr_decay(float2 sr, float2 rate)
+{
+    Decay2 g;
+    g.l = __fmul2_rn(rate, sr);
+    const float2 p = one_minus_exp<Near>(g.l);
+    g.a = __fadd2_rn(both(1.0f), neg(p));
+    g.q = __fmul2_rn(p, __fadd2_rn(both(2.0f), neg(p)));
+    return g;
+}
+
+// a and b = m s(i) x of one row
+template <bool Near>
+__device__ __forceinline__ void glr_row(float2 r, float2 i, float2 x, float2 rate, float2& a, float2& b)
+{
+    const Decay2 g = glr_decay<Near>(logistic(r), rate);
+    a = g.a;
+    b = __fmul2_rn(__fmul2_rn(make_float2(sqrt_approx(g.q.x), sqrt_approx(g.q.y)), logistic(i)), x);
 }
 
 // ------------------------------------------------- sequences in packed rows
@@ -105,14 +132,14 @@ __device__ __forceinline__ RowSeq row_seq(const int* starts, int T, int n_seq, i
 }
 
 // Sequences without rows: `out` gets `in` (or zeros).  The CTAs of the grid
-// share them.
+// share them; called by a CTA's first 256 threads.
 __device__ __forceinline__ void copy_empty(const int* starts, int T, int n_seq, long long D, const float* in, float* out)
 {
     if (!starts || !out) return;
     for (int s = blockIdx.x; s < n_seq; s += gridDim.x) {
         const int lo = min(max(__ldg(starts + s), 0), T);
         if (min(max(__ldg(starts + s + 1), lo), T) > lo) continue;
-        for (long long d = threadIdx.x; d < D; d += blockDim.x) out[s * D + d] = in ? in[s * D + d] : 0.f;
+        for (long long d = threadIdx.x; d < D; d += 256) out[s * D + d] = in ? in[s * D + d] : 0.f;
     }
 }
 
@@ -129,13 +156,25 @@ __device__ __forceinline__ void copy_empty(const int* starts, int T, int n_seq, 
 // as it has read the tile, and finds the state entering its next tile by
 // applying the P - 1 maps of the tiles between to the state that its own last
 // tile ended with: no chain of CTAs waiting for one another's states, and a
-// fixed order of operations (the same bits every run).  Warp w of a CTA takes
-// rows w kRows .. of a tile, lane l channels 2 l and 2 l + 1.
+// fixed order of operations (the same bits every run).
+//
+// Warps 0..7 of a CTA compute: warp w takes rows w kRows .. of a tile, lane l
+// channels 2 l and 2 l + 1.  They fold tile n + 1 before they run through tile
+// n, so that the way of a map to the other CTAs and of theirs to here (two
+// trips to L2, more than a microsecond) passes behind a tile's work.  Warp 8
+// loads the tiles (four stages, TMA), joins the warps' maps, publishes, looks
+// up the others' and hands each warp the state entering its rows.
+//
+// A published map needs no flag: the maps' memory starts as words of all ones,
+// a written word is never that, and a reader takes a map when none of its
+// words is.  The sign of A (a product of decays, not negative) says whether
+// the tile holds a cut.
 
 constexpr int kGD = 64;        // channels of a slab
-constexpr int kGWarps = 8;
-constexpr int kGThreads = 32 * kGWarps;
-constexpr int kGMaxP = 33;     // CTAs of a slab: one lane for each of the others
+constexpr int kGWarps = 8;     // that compute
+constexpr int kGThreads = 32 * (kGWarps + 1);
+constexpr int kGStages = 4;
+constexpr int kGMaxP = 33;     // most CTAs of a slab
 
 struct GlrParams {
     const float *rate, *h0;
@@ -146,12 +185,11 @@ struct GlrParams {
     long long D;
     int T, n_seq, L, S, P, tiles;
     WsHeader* hdr;
-    unsigned* flags;  // [tiles][S]: 0, or 1 + whether the tile holds a cut
-    float4* maps;     // [tiles][S][32]: (A, B) of channel 2 l, of 2 l + 1
+    uint4* maps;      // [tiles][S][32]: (A, B) of channel 2 l, of 2 l + 1
     unsigned long long wait_ns;
 };
 
-// One channel pair's map y -> A y + B, or y -> B (cut).
+// One channel pair's map y -> a y + b, or y -> b (cut).
 struct Map2 {
     float2 a, b;
     bool cut;
@@ -159,88 +197,117 @@ struct Map2 {
 
 __device__ __forceinline__ float2 apply(const Map2& m, float2 y)
 {
-    return m.cut ? m.b : make_float2(fmaf(m.a.x, y.x, m.b.x), fmaf(m.a.y, y.y, m.b.y));
+    return m.cut ? m.b : __ffma2_rn(m.a, y, m.b);
 }
 
 // The shared parts of both scans' shared memory behind the stages.
 struct GlrShared {
-    float4 agg[kGWarps][32];   // the warps' maps
-    float2 enter[kGWarps][32]; // the state entering each warp's rows
-    int cut[kGWarps];
-    int failed;
-    uint64_t full[2];
+    float4 agg[2][kGWarps][32];   // the warps' maps, by the tile's parity
+    float2 enter[2][kGWarps][32]; // the state entering each warp's rows
+    int cut[2][kGWarps];
+    uint64_t full[kGStages], empty[kGStages];
+    uint64_t agg_full[2], entered[2];
 };
 
-// Warp 0, after the warps' maps are in sh.agg: the tile's map to the other
-// CTAs, the state entering the tile, and from it that entering each warp's
-// rows.  `own` is the state the CTA's last tile ended with; it becomes this
-// tile's.  W(i) is the warp that comes i-th in the scan's direction.
+__device__ __forceinline__ void glr_init(GlrShared& sh)
+{
+    for (int i = 0; i < kGStages; ++i) {
+        mbar_init(&sh.full[i], 1);
+        mbar_init(&sh.empty[i], kGWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+        mbar_init(&sh.agg_full[i], kGWarps);
+        mbar_init(&sh.entered[i], 1);
+    }
+    fence_mbar_init();
+}
+
+// The bits of a published word: never all ones.
+__device__ __forceinline__ unsigned map_word(float x)
+{
+    const unsigned u = __float_as_uint(x);
+    return x != x ? 0x7fc00000u : u;
+}
+
+__device__ __forceinline__ uint4 ld_map(const uint4* p)
+{
+    uint4 v;
+    asm volatile("ld.volatile.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+// The control warp, with the warps' maps of tile k (the CTA's n-th) in shared
+// memory: publishes the tile's map, finds the state entering the tile (`own`
+// is the state the CTA's last tile ended with; it becomes this one's) and from
+// it the state entering each warp's rows.  False when a wait ran out.
 template <bool Reverse>
-__device__ __forceinline__ void glr_carry(const GlrParams& p, GlrShared& sh, int slab, int k, int lane, float2& own)
+__device__ __forceinline__ bool glr_carry(const GlrParams& p, GlrShared& sh, int slab, int k, int n, int lane, float2& own)
 {
     auto warp_at = [](int i) { return Reverse ? kGWarps - 1 - i : i; };
+    const int par = n & 1;
     Map2 m[kGWarps];
 #pragma unroll
     for (int i = 0; i < kGWarps; ++i) {
-        const float4 v = sh.agg[warp_at(i)][lane];
-        m[i] = Map2{make_float2(v.x, v.z), make_float2(v.y, v.w), sh.cut[warp_at(i)] != 0};
+        const float4 v = sh.agg[par][warp_at(i)][lane];
+        m[i] = Map2{make_float2(v.x, v.z), make_float2(v.y, v.w), sh.cut[par][warp_at(i)] != 0};
     }
-    bool ok = true;
     if (p.P > 1) {
         Map2 all = m[0];
 #pragma unroll
         for (int i = 1; i < kGWarps; ++i) {
             all.b = apply(m[i], all.b);
-            all.a = make_float2(m[i].a.x * all.a.x, m[i].a.y * all.a.y);
+            all.a = __fmul2_rn(m[i].a, all.a);
             all.cut |= m[i].cut;
         }
-        const size_t at = size_t(k) * p.S + slab;
-        __stcg(p.maps + at * 32 + lane, make_float4(all.a.x, all.b.x, all.a.y, all.b.y));
-        __threadfence();
-        __syncwarp();
-        if (lane == 0)
-            asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(p.flags + at), "r"(all.cut ? 2u : 1u) : "memory");
+        uint4 out = make_uint4(map_word(all.a.x), map_word(all.b.x), map_word(all.a.y), map_word(all.b.y));
+        out.x = all.cut ? out.x | 0x80000000u : out.x & 0x7fffffffu;
+        uint4* to = p.maps + (size_t(k) * p.S + slab) * 32 + lane;
+        asm volatile("st.volatile.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(to), "r"(out.x), "r"(out.y), "r"(out.z),
+                     "r"(out.w)
+                     : "memory");
         // the tiles since this CTA's last one (all of them in its first turn)
-        const int first = max(k - p.P + 1, 0), n = k - first;
-        unsigned f = 1;
-        if (lane < n) {
-            const unsigned* q = p.flags + size_t(first + lane) * p.S + slab;
-            f = ld_acquire_gpu_u32(q);
-            if (f == 0) {
-                const long long t0 = clock64();
-                while ((f = ld_acquire_gpu_u32(q)) == 0) {
-                    if (clock64() - t0 > (long long)(2 * p.wait_ns) || error_raised(&p.hdr->error)) {
-                        raise_error(&p.hdr->error, PARARNN_ERR_TIMEOUT);
-                        break;
-                    }
+        const int first = max(k - p.P + 1, 0), cnt = k - first;
+        const uint4* from = p.maps + (size_t(first) * p.S + slab) * 32 + lane;
+        for (int i = 0; i < cnt; i += 8) {
+            uint4 v[8];
+            long long t0 = 0;
+            for (;;) {
+                bool there = true;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = i + j < cnt ? ld_map(from + size_t(i + j) * p.S * 32) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    there = there && v[j].x != ~0u && v[j].y != ~0u && v[j].z != ~0u && v[j].w != ~0u;
+                if (__all_sync(0xffffffffu, there)) break;
+                if (t0 == 0) t0 = clock64();
+                const bool late = clock64() - t0 > (long long)(2 * p.wait_ns);
+                if (__any_sync(0xffffffffu, late || error_raised(&p.hdr->error))) {
+                    raise_error(&p.hdr->error, PARARNN_ERR_TIMEOUT);
+                    return false;
                 }
             }
-        }
-        ok = __all_sync(0xffffffffu, f != 0);
-        const unsigned cuts = __ballot_sync(0xffffffffu, lane < n && f == 2);
-        if (ok) {
-            // nothing before the last cut matters
-            int i = cuts ? 31 - __clz(cuts) : 0;
-            for (; i < n; i += 8) {
-                float4 v[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (i + j < n) v[j] = __ldcg(p.maps + (size_t(first + i + j) * p.S + slab) * 32 + lane);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (i + j < n)
-                        own = apply(Map2{make_float2(v[j].x, v[j].z), make_float2(v[j].y, v[j].w),
-                                         ((cuts >> (i + j)) & 1u) != 0},
-                                    own);
+            for (int j = 0; j < 8; ++j) {
+                if (i + j < cnt) {
+                    const bool cut = v[j].x >> 31;
+                    own = apply(Map2{make_float2(__uint_as_float(v[j].x & 0x7fffffffu), __uint_as_float(v[j].z)),
+                                     make_float2(__uint_as_float(v[j].y), __uint_as_float(v[j].w)), cut},
+                                own);
+                }
             }
         }
     }
 #pragma unroll
     for (int i = 0; i < kGWarps; ++i) {
-        sh.enter[warp_at(i)][lane] = own;
+        sh.enter[par][warp_at(i)][lane] = own;
         own = apply(m[i], own);
     }
-    if (lane == 0 && !ok) sh.failed = 1;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.entered[par]);
+    return true;
 }
 
 template <class UT>
@@ -250,139 +317,163 @@ __device__ __forceinline__ float2 pair_of(const UT* p)
     return make_float2(v.v[0], v.v[1]);
 }
 
+// What a warp has to know of its rows: bit i for row i, the owners in the lanes.
+struct RowMasks {
+    unsigned firsts, lasts, mine;
+    int owner;
+};
+
+__device__ __forceinline__ RowMasks row_masks(const GlrParams& p, int t0, int rows, int lane)
+{
+    const RowSeq rs = row_seq(p.starts, p.T, p.n_seq, p.L, lane < rows ? t0 + lane : -1);
+    RowMasks m;
+    m.firsts = __ballot_sync(0xffffffffu, rs.first);
+    m.lasts = __ballot_sync(0xffffffffu, rs.last);
+    m.mine = __ballot_sync(0xffffffffu, rs.owner >= 0);
+    m.owner = rs.owner;
+    return m;
+}
+
 template <class UT>
 struct GlrScanLayout {
-    static constexpr int kRows = sizeof(UT) == 2 ? 16 : 8;  // of a warp
+    static constexpr int kRows = sizeof(UT) == 2 ? 12 : 8;  // of a warp
     static constexpr int kTile = kRows * kGWarps;
     static constexpr size_t stage_bytes = size_t(kTile) * 3 * kGD * sizeof(UT);
-    static constexpr size_t smem_bytes = 2 * stage_bytes + sizeof(GlrShared) + 128;
+    static constexpr size_t smem_bytes = kGStages * stage_bytes + sizeof(GlrShared) + 128;
+    static_assert(smem_bytes <= 232448, "shared memory");
 };
 
 template <class UT>
-__global__ void __launch_bounds__(kGThreads, 2) glr_scan_kernel(const __grid_constant__ CUtensorMap tm_u, const GlrParams p)
+__global__ void __launch_bounds__(kGThreads, 1) glr_scan_kernel(const __grid_constant__ CUtensorMap tm_u, const GlrParams p)
 {
     using LY = GlrScanLayout<UT>;
     constexpr int R = LY::kRows;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
-    GlrShared& sh = *reinterpret_cast<GlrShared*>(smem + 2 * LY::stage_bytes);
+    GlrShared& sh = *reinterpret_cast<GlrShared*>(smem + kGStages * LY::stage_bytes);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slab = blockIdx.x % p.S, turn = blockIdx.x / p.S;
     const int d = slab * kGD + 2 * lane;
     const bool in = d < p.D;
+    const int mine = turn < p.tiles ? (p.tiles - 1 - turn) / p.P + 1 : 0;  // tiles turn, turn + P, ..
+    int* err = &p.hdr->error;
     if (threadIdx.x == 0) {
         if (p.P == 1 && blockIdx.x == 0) clear_outcome(p.hdr);
-        sh.failed = 0;
-        mbar_init(&sh.full[0], 1);
-        mbar_init(&sh.full[1], 1);
-        fence_mbar_init();
+        glr_init(sh);
     }
     __syncthreads();
-    auto load = [&](int k, int s) {
-        mbar_arrive_expect_tx(&sh.full[s], uint32_t(LY::stage_bytes));
-        tma_load_3d(smem + s * LY::stage_bytes, &tm_u, slab * kGD, 0, k * LY::kTile, &sh.full[s]);
-    };
-    if (threadIdx.x == 0) {
-        if (turn < p.tiles) load(turn, 0);
-        if (turn + p.P < p.tiles) load(turn + p.P, 1);
-    }
-    copy_empty(p.starts, p.T, p.n_seq, p.D, p.h0, p.h_last);
-    const float2 rate = in ? pair_of(p.rate + d) : make_float2(0.f, 0.f);
-    float2 own = make_float2(0.f, 0.f);  // warp 0's: the state this CTA's last tile ended with
     bool ok = true;
-    int n = 0;
-    for (int k = turn; k < p.tiles; k += p.P, ++n) {
-        const int s = n & 1, t0 = k * LY::kTile + w * R;
-        // this warp's rows: lane i looks at row i
-        const RowSeq rs = row_seq(p.starts, p.T, p.n_seq, p.L, lane < R ? t0 + lane : -1);
-        const unsigned firsts = __ballot_sync(0xffffffffu, rs.first), lasts = __ballot_sync(0xffffffffu, rs.last);
-        const unsigned mine = __ballot_sync(0xffffffffu, rs.owner >= 0);
-        ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.full[s], uint32_t(n >> 1) & 1u, &p.hdr->error, p.wait_ns));
-        const UT* src = reinterpret_cast<const UT*>(smem + s * LY::stage_bytes) + size_t(w) * R * 3 * kGD + 2 * lane;
-        float2 a[R], b[R];
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const float2 r = pair_of(src + i * 3 * kGD), g = pair_of(src + (i * 3 + 1) * kGD),
-                         x = pair_of(src + (i * 3 + 2) * kGD);
-            const GlrStep g0 = glr_gates(r.x, g.x, rate.x), g1 = glr_gates(r.y, g.y, rate.y);
-            a[i] = make_float2(g0.a, g1.a);
-            b[i] = make_float2(sqrt_approx(g0.q) * g0.si * x.x, sqrt_approx(g1.q) * g1.si * x.y);
+    if (w == kGWarps) {
+        auto load = [&](int n) {
+            const int s = n % kGStages;
+            mbar_arrive_expect_tx(&sh.full[s], uint32_t(LY::stage_bytes));
+            tma_load_3d(smem + s * LY::stage_bytes, &tm_u, slab * kGD, 0, (turn + n * p.P) * LY::kTile, &sh.full[s]);
+        };
+        if (lane == 0)
+            for (int n = 0; n < min(mine, kGStages); ++n) load(n);
+        float2 own = make_float2(0.f, 0.f);
+        for (int n = 0; n < mine && ok; ++n) {
+            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.agg_full[n & 1], uint32_t(n >> 1) & 1u, err, p.wait_ns));
+            if (!ok) break;
+            if (lane == 0 && n + kGStages < mine) load(n + kGStages);  // every warp has read the stage
+            ok = glr_carry<false>(p, sh, slab, turn + n * p.P, n, lane, own);
         }
-        if (firsts) {  // the states before the sequences that start here
+    } else {
+        const float2 rate = in ? pair_of(p.rate + d) : make_float2(0.f, 0.f);
+        const bool near = __all_sync(0xffffffffu, rate.x < 0.25f && rate.y < 0.25f);
+        // fold tile n: its rows' a and b into registers, the warp's map out
+        auto fold = [&](int n, float2(&a)[R], float2(&b)[R], RowMasks& rm) {
+            const int s = n % kGStages;
+            rm = row_masks(p, (turn + n * p.P) * LY::kTile + w * R, R, lane);
+            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.full[s], uint32_t(n / kGStages) & 1u, err, p.wait_ns));
+            const UT* src = reinterpret_cast<const UT*>(smem + s * LY::stage_bytes) + size_t(w) * R * 3 * kGD + 2 * lane;
+            auto rows = [&](auto is_near) {
 #pragma unroll
-            for (int i = 0; i < R; ++i)
-                if ((firsts >> i) & 1u) {
-                    const long long o = __shfl_sync(0xffffffffu, rs.owner, i);
-                    if (p.h0 && in) {
-                        const float2 h = pair_of(p.h0 + o * p.D + d);
-                        b[i] = make_float2(fmaf(a[i].x, h.x, b[i].x), fmaf(a[i].y, h.y, b[i].y));
-                    }
+                for (int i = 0; i < R; ++i)
+                    glr_row<decltype(is_near)::value>(pair_of(src + i * 3 * kGD), pair_of(src + (i * 3 + 1) * kGD),
+                                                      pair_of(src + (i * 3 + 2) * kGD), rate, a[i], b[i]);
+            };
+            if (near) rows(std::true_type());
+            else rows(std::false_type());
+            float2 A = both(1.f), B = both(0.f);
+            if (rm.firsts == 0) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    B = __ffma2_rn(a[i], B, b[i]);
+                    A = __fmul2_rn(A, a[i]);
                 }
-        }
-        float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
+            } else {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const bool cut = (firsts >> i) & 1u;
-            B = apply(Map2{a[i], b[i], cut}, B);
-            A = make_float2(A.x * a[i].x, A.y * a[i].y);
-        }
-        sh.agg[w][lane] = make_float4(A.x, B.x, A.y, B.y);
-        if (lane == 0) sh.cut[w] = firsts != 0;
-        ok = !__syncthreads_or(!ok);  // the stage is read, the maps are there
-        if (!ok) break;
-        if (threadIdx.x == 0 && k + 2 * p.P < p.tiles) load(k + 2 * p.P, s);
-        if (w == 0) glr_carry<false>(p, sh, slab, k, lane, own);
-        __syncthreads();
-        if (sh.failed) {  // written between the two barriers alone
-            ok = false;
-            break;
-        }
-        float2 y = sh.enter[w][lane];
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            y = apply(Map2{a[i], b[i], ((firsts >> i) & 1u) != 0}, y);
-            if (in && ((mine >> i) & 1u)) *reinterpret_cast<float2*>(p.h + (long long)(t0 + i) * p.D + d) = y;
-            if ((lasts >> i) & 1u) {
-                const long long o = __shfl_sync(0xffffffffu, rs.owner, i);
-                if (p.h_last && in) *reinterpret_cast<float2*>(p.h_last + o * p.D + d) = y;
+                for (int i = 0; i < R; ++i) {
+                    const bool cut = (rm.firsts >> i) & 1u;
+                    const long long o = __shfl_sync(0xffffffffu, rm.owner, i);
+                    if (cut && p.h0 && in) b[i] = __ffma2_rn(a[i], pair_of(p.h0 + o * p.D + d), b[i]);
+                    B = apply(Map2{a[i], b[i], cut}, B);
+                    A = __fmul2_rn(A, a[i]);
+                }
             }
+            sh.agg[n & 1][w][lane] = make_float4(A.x, B.x, A.y, B.y);
+            if (lane == 0) sh.cut[n & 1][w] = rm.firsts != 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.agg_full[n & 1]);
+        };
+        // run through tile n from the state entering this warp's rows
+        auto finish = [&](int n, const float2(&a)[R], const float2(&b)[R], const RowMasks& rm) {
+            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.entered[n & 1], uint32_t(n >> 1) & 1u, err, p.wait_ns));
+            if (!ok) return;
+            const int t0 = (turn + n * p.P) * LY::kTile + w * R;
+            float2 y = sh.enter[n & 1][w][lane];
+            float* h = p.h + (long long)t0 * p.D + d;
+            if (rm.firsts == 0 && rm.lasts == 0 && rm.mine == (1u << R) - 1u) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    y = __ffma2_rn(a[i], y, b[i]);
+                    if (in) *reinterpret_cast<float2*>(h) = y;
+                    h += p.D;
+                }
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                y = apply(Map2{a[i], b[i], ((rm.firsts >> i) & 1u) != 0}, y);
+                if (in && ((rm.mine >> i) & 1u)) *reinterpret_cast<float2*>(h + i * p.D) = y;
+                if ((rm.lasts >> i) & 1u) {
+                    const long long o = __shfl_sync(0xffffffffu, rm.owner, i);
+                    if (p.h_last && in) *reinterpret_cast<float2*>(p.h_last + o * p.D + d) = y;
+                }
+            }
+        };
+        float2 a0[R], b0[R], a1[R], b1[R];
+        RowMasks m0, m1;
+        if (mine > 0) fold(0, a0, b0, m0);
+        for (int n = 0; n < mine && ok; n += 2) {
+            if (n + 1 < mine) fold(n + 1, a1, b1, m1);
+            if (ok) finish(n, a0, b0, m0);
+            if (!ok || n + 1 >= mine) break;
+            if (n + 2 < mine) fold(n + 2, a0, b0, m0);
+            if (ok) finish(n + 1, a1, b1, m1);
         }
+        copy_empty(p.starts, p.T, p.n_seq, p.D, p.h0, p.h_last);
     }
     if (!ok) let_copies_land();
 }
 
-struct GlrGrad {
-    float dr, di, dx, ds;
-};
-
-__device__ __forceinline__ GlrGrad glr_grad(const GlrStep& g, float x, float before, float lam)
-{
-    // where l = 0 (a shut gate) the square root has no slope: its term is 0
-    const float im = g.q > 1e-37f ? rsqrt_approx(g.q) : 0.f;
-    GlrGrad o;
-    o.dx = lam * (g.q * im) * g.si;
-    o.di = o.dx * x * (1.0f - g.si);
-    const float dl = lam * (g.si * x * (g.a * g.a * im) - g.a * before);
-    o.dr = dl * g.l * (1.0f - g.sr);
-    o.ds = dl * g.sr;
-    return o;
-}
-
 template <class UT>
 struct GlrAdjointLayout {
-    static constexpr int kRows = sizeof(UT) == 2 ? 7 : 5;  // of a warp: two CTAs of two stages on an SM
+    static constexpr int kRows = sizeof(UT) == 2 ? 7 : 5;  // of a warp
     static constexpr int kTile = kRows * kGWarps;
     static constexpr size_t u_bytes = size_t(kTile) * 3 * kGD * sizeof(UT), f_bytes = size_t(kTile) * kGD * 4;
     static constexpr size_t stage_bytes = u_bytes + 2 * f_bytes;
-    static constexpr size_t smem_bytes = 2 * stage_bytes + sizeof(GlrShared) + 128;
+    static constexpr size_t smem_bytes = kGStages * stage_bytes + sizeof(GlrShared) + 128;
+    static_assert(smem_bytes <= 232448, "shared memory");
 };
 
 // Tiles are counted from the last row: tile k holds rows T - (k + 1) kTile ..
 // T - k kTile - 1 (tile after tile towards the first row; the last tile may
-// start before row 0, where there is nothing).  The stage stays until the
-// second sweep has read it again.
+// start before row 0, where there is nothing).  A stage stays until its tile
+// has been run through.
 template <class UT>
-__global__ void __launch_bounds__(kGThreads, 2)
+__global__ void __launch_bounds__(kGThreads, 1)
     glr_adjoint_kernel(const __grid_constant__ CUtensorMap tm_u, const __grid_constant__ CUtensorMap tm_h,
                        const __grid_constant__ CUtensorMap tm_dh, const GlrParams p)
 {
@@ -390,119 +481,153 @@ __global__ void __launch_bounds__(kGThreads, 2)
     constexpr int R = LY::kRows;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
-    GlrShared& sh = *reinterpret_cast<GlrShared*>(smem + 2 * LY::stage_bytes);
+    GlrShared& sh = *reinterpret_cast<GlrShared*>(smem + kGStages * LY::stage_bytes);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slab = blockIdx.x % p.S, turn = blockIdx.x / p.S;
     const int d = slab * kGD + 2 * lane;
     const bool in = d < p.D;
+    const int mine = turn < p.tiles ? (p.tiles - 1 - turn) / p.P + 1 : 0;
+    int* err = &p.hdr->error;
     if (threadIdx.x == 0) {
         if (p.P == 1 && blockIdx.x == 0) clear_outcome(p.hdr);
-        sh.failed = 0;
-        mbar_init(&sh.full[0], 1);
-        mbar_init(&sh.full[1], 1);
-        fence_mbar_init();
+        glr_init(sh);
     }
     __syncthreads();
-    auto load = [&](int k, int s) {
-        unsigned char* to = smem + s * LY::stage_bytes;
-        const int t = p.T - (k + 1) * LY::kTile;
-        mbar_arrive_expect_tx(&sh.full[s], uint32_t(LY::stage_bytes));
-        tma_load_3d(to, &tm_u, slab * kGD, 0, t, &sh.full[s]);
-        tma_load_2d(to + LY::u_bytes, &tm_h, slab * kGD, t - 1, &sh.full[s]);  // the states before the rows
-        tma_load_2d(to + LY::u_bytes + LY::f_bytes, &tm_dh, slab * kGD, t, &sh.full[s]);
-    };
-    if (threadIdx.x == 0) {
-        if (turn < p.tiles) load(turn, 0);
-        if (turn + p.P < p.tiles) load(turn + p.P, 1);
-    }
-    copy_empty(p.starts, p.T, p.n_seq, p.D, p.dh_last, p.dh0);
-    const float2 rate = in ? pair_of(p.rate + d) : make_float2(0.f, 0.f);
-    float2 own = make_float2(0.f, 0.f), ds = make_float2(0.f, 0.f);
     bool ok = true;
-    int n = 0;
-    for (int k = turn; k < p.tiles; k += p.P, ++n) {
-        const int s = n & 1, t0 = p.T - (k + 1) * LY::kTile + w * R;
-        const RowSeq rs = row_seq(p.starts, p.T, p.n_seq, p.L, lane < R ? t0 + lane : -1);
-        const unsigned firsts = __ballot_sync(0xffffffffu, rs.first), lasts = __ballot_sync(0xffffffffu, rs.last);
-        const unsigned mine = __ballot_sync(0xffffffffu, rs.owner >= 0);
-        ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.full[s], uint32_t(n >> 1) & 1u, &p.hdr->error, p.wait_ns));
-        const unsigned char* stage = smem + s * LY::stage_bytes;
-        const UT* su = reinterpret_cast<const UT*>(stage) + size_t(w) * R * 3 * kGD + 2 * lane;
-        const float* sb = reinterpret_cast<const float*>(stage + LY::u_bytes) + w * R * kGD + 2 * lane;
-        const float* sd = reinterpret_cast<const float*>(stage + LY::u_bytes + LY::f_bytes) + w * R * kGD + 2 * lane;
+    float2 ds = make_float2(0.f, 0.f);
+    if (w == kGWarps) {
+        auto load = [&](int n) {
+            const int s = n % kGStages, t = p.T - (turn + n * p.P + 1) * LY::kTile;
+            unsigned char* to = smem + s * LY::stage_bytes;
+            mbar_arrive_expect_tx(&sh.full[s], uint32_t(LY::stage_bytes));
+            tma_load_3d(to, &tm_u, slab * kGD, 0, t, &sh.full[s]);
+            tma_load_2d(to + LY::u_bytes, &tm_h, slab * kGD, t - 1, &sh.full[s]);  // the states before the rows
+            tma_load_2d(to + LY::u_bytes + LY::f_bytes, &tm_dh, slab * kGD, t, &sh.full[s]);
+        };
+        if (lane == 0)
+            for (int n = 0; n < min(mine, kGStages); ++n) load(n);
+        float2 own = make_float2(0.f, 0.f);
+        for (int n = 0; n < mine && ok; ++n) {
+            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.agg_full[n & 1], uint32_t(n >> 1) & 1u, err, p.wait_ns));
+            if (!ok) break;
+            ok = glr_carry<true>(p, sh, slab, turn + n * p.P, n, lane, own);
+            // the warps run through tile n - 1 before they fold tile n + 1
+            if (ok && n > 0 && n - 1 + kGStages < mine) {
+                const int s = (n - 1) % kGStages;
+                ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.empty[s], uint32_t((n - 1) / kGStages) & 1u, err, p.wait_ns));
+                if (ok && lane == 0) load(n - 1 + kGStages);
+            }
+        }
+    } else {
+        const float2 rate = in ? pair_of(p.rate + d) : make_float2(0.f, 0.f);
+        const bool near = __all_sync(0xffffffffu, rate.x < 0.25f && rate.y < 0.25f);
         // G = a (up + G of the row behind): the map of a row is (a, a up)
-        float2 sr[R], up[R];
-        float2 A = make_float2(1.f, 1.f), B = make_float2(0.f, 0.f);
+        auto fold = [&](int n, float2(&sr)[R], float2(&up)[R], RowMasks& rm) {
+            const int s = n % kGStages;
+            rm = row_masks(p, p.T - (turn + n * p.P + 1) * LY::kTile + w * R, R, lane);
+            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.full[s], uint32_t(n / kGStages) & 1u, err, p.wait_ns));
+            const unsigned char* stage = smem + s * LY::stage_bytes;
+            const UT* su = reinterpret_cast<const UT*>(stage) + size_t(w) * R * 3 * kGD + 2 * lane;
+            const float* sd = reinterpret_cast<const float*>(stage + LY::u_bytes + LY::f_bytes) + w * R * kGD + 2 * lane;
 #pragma unroll
-        for (int i = R - 1; i >= 0; --i) {
-            const float2 r = pair_of(su + i * 3 * kGD);
-            sr[i] = make_float2(logistic(r.x), logistic(r.y));
-            up[i] = pair_of(sd + i * kGD);
-            const bool cut = (lasts >> i) & 1u;
-            if (cut && p.dh_last) {
-                const long long o = __shfl_sync(0xffffffffu, rs.owner, i);
-                if (in) {
-                    const float2 e = pair_of(p.dh_last + o * p.D + d);
-                    up[i] = make_float2(up[i].x + e.x, up[i].y + e.y);
+            for (int i = 0; i < R; ++i) {
+                sr[i] = logistic(pair_of(su + i * 3 * kGD));
+                up[i] = pair_of(sd + i * kGD);
+            }
+            if (rm.lasts && p.dh_last) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const long long o = __shfl_sync(0xffffffffu, rm.owner, i);
+                    if (((rm.lasts >> i) & 1u) && in) up[i] = __fadd2_rn(up[i], pair_of(p.dh_last + o * p.D + d));
                 }
             }
-            const float2 a = make_float2(1.0f - one_minus_exp(rate.x * sr[i].x), 1.0f - one_minus_exp(rate.y * sr[i].y));
-            B = apply(Map2{a, make_float2(a.x * up[i].x, a.y * up[i].y), cut}, B);
-            A = make_float2(A.x * a.x, A.y * a.y);
-        }
-        sh.agg[w][lane] = make_float4(A.x, B.x, A.y, B.y);
-        if (lane == 0) sh.cut[w] = lasts != 0;
-        ok = !__syncthreads_or(!ok);
-        if (!ok) break;
-        if (w == 0) glr_carry<true>(p, sh, slab, k, lane, own);
-        __syncthreads();
-        if (sh.failed) {
-            ok = false;
-            break;
-        }
-        float2 G = sh.enter[w][lane];
+            float2 A = both(1.f), B = both(0.f);
+            auto rows = [&](auto is_near) {
 #pragma unroll
-        for (int i = R - 1; i >= 0; --i) {
-            const float2 g = pair_of(su + (i * 3 + 1) * kGD), x = pair_of(su + (i * 3 + 2) * kGD);
-            float2 before = pair_of(sb + i * kGD);
-            if ((firsts >> i) & 1u) {
-                const long long o = __shfl_sync(0xffffffffu, rs.owner, i);
-                before = p.h0 && in ? pair_of(p.h0 + o * p.D + d) : make_float2(0.f, 0.f);
-            }
-            const bool cut = (lasts >> i) & 1u;
-            const float2 lam = cut ? up[i] : make_float2(up[i].x + G.x, up[i].y + G.y);
-            const GlrStep s0 = glr_open(sr[i].x, g.x, rate.x), s1 = glr_open(sr[i].y, g.y, rate.y);
-            G = make_float2(s0.a * lam.x, s1.a * lam.y);
-            if (!((mine >> i) & 1u)) continue;
-            const GlrGrad o0 = glr_grad(s0, x.x, before.x, lam.x), o1 = glr_grad(s1, x.y, before.y, lam.y);
-            ds.x += o0.ds;
-            ds.y += o1.ds;
-            if (in) {
-                float* q = p.du + (long long)(t0 + i) * 3 * p.D + d;
-                *reinterpret_cast<float2*>(q) = make_float2(o0.dr, o1.dr);
-                *reinterpret_cast<float2*>(q + p.D) = make_float2(o0.di, o1.di);
-                *reinterpret_cast<float2*>(q + 2 * p.D) = make_float2(o0.dx, o1.dx);
-            }
-            if ((firsts >> i) & 1u) {
-                const long long o = __shfl_sync(0xffffffffu, rs.owner, i);
-                if (p.dh0 && in) *reinterpret_cast<float2*>(p.dh0 + o * p.D + d) = G;
-            }
+                for (int i = R - 1; i >= 0; --i) {
+                    const float2 a = glr_decay<decltype(is_near)::value>(sr[i], rate).a;
+                    const bool cut = (rm.lasts >> i) & 1u;
+                    B = __fmul2_rn(a, cut ? up[i] : __fadd2_rn(up[i], B));
+                    A = __fmul2_rn(A, a);
+                }
+            };
+            if (near) rows(std::true_type());
+            else rows(std::false_type());
+            sh.agg[n & 1][w][lane] = make_float4(A.x, B.x, A.y, B.y);
+            if (lane == 0) sh.cut[n & 1][w] = rm.lasts != 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.agg_full[n & 1]);
+        };
+        auto finish = [&](int n, const float2(&sr)[R], const float2(&up)[R], const RowMasks& rm) {
+            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.entered[n & 1], uint32_t(n >> 1) & 1u, err, p.wait_ns));
+            if (!ok) return;
+            const int s = n % kGStages, t0 = p.T - (turn + n * p.P + 1) * LY::kTile + w * R;
+            const unsigned char* stage = smem + s * LY::stage_bytes;
+            const UT* su = reinterpret_cast<const UT*>(stage) + size_t(w) * R * 3 * kGD + 2 * lane;
+            const float* sb = reinterpret_cast<const float*>(stage + LY::u_bytes) + w * R * kGD + 2 * lane;
+            float2 G = sh.enter[n & 1][w][lane];
+            auto rows = [&](auto is_near) {
+#pragma unroll
+                for (int i = R - 1; i >= 0; --i) {
+                    const float2 si = logistic(pair_of(su + (i * 3 + 1) * kGD)), x = pair_of(su + (i * 3 + 2) * kGD);
+                    float2 before = pair_of(sb + i * kGD);
+                    if ((rm.firsts >> i) & 1u) {
+                        const long long o = __shfl_sync(0xffffffffu, rm.owner, i);
+                        before = p.h0 && in ? pair_of(p.h0 + o * p.D + d) : both(0.f);
+                    }
+                    const float2 lam = (rm.lasts >> i) & 1u ? up[i] : __fadd2_rn(up[i], G);
+                    const Decay2 g = glr_decay<decltype(is_near)::value>(sr[i], rate);
+                    G = __fmul2_rn(g.a, lam);
+                    if (!((rm.mine >> i) & 1u)) continue;
+                    // 1 / m; where l = 0 (a shut gate) the root has no slope: its terms are 0
+                    const float2 im = make_float2(g.q.x > 1e-37f ? rsqrt_approx(g.q.x) : 0.f,
+                                                  g.q.y > 1e-37f ? rsqrt_approx(g.q.y) : 0.f);
+                    const float2 lsi = __fmul2_rn(lam, si);
+                    const float2 dx = __fmul2_rn(lsi, __fmul2_rn(g.q, im));
+                    const float2 di = __fmul2_rn(__fmul2_rn(dx, x), __fadd2_rn(both(1.f), neg(si)));
+                    // dl = lam (s(i) x a^2 / m - a h)
+                    const float2 in_m = __fmul2_rn(__fmul2_rn(__fmul2_rn(lsi, x), __fmul2_rn(g.a, g.a)), im);
+                    const float2 dl = __ffma2_rn(neg(G), before, in_m);
+                    const float2 dr = __fmul2_rn(__fmul2_rn(dl, g.l), __fadd2_rn(both(1.f), neg(sr[i])));
+                    ds = __ffma2_rn(dl, sr[i], ds);
+                    if (in) {
+                        float* q = p.du + (long long)(t0 + i) * 3 * p.D + d;
+                        *reinterpret_cast<float2*>(q) = dr;
+                        *reinterpret_cast<float2*>(q + p.D) = di;
+                        *reinterpret_cast<float2*>(q + 2 * p.D) = dx;
+                    }
+                    if ((rm.firsts >> i) & 1u) {
+                        const long long o = __shfl_sync(0xffffffffu, rm.owner, i);
+                        if (p.dh0 && in) *reinterpret_cast<float2*>(p.dh0 + o * p.D + d) = G;
+                    }
+                }
+            };
+            if (near) rows(std::true_type());
+            else rows(std::false_type());
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.empty[s]);
+        };
+        float2 s0[R], u0[R], s1[R], u1[R];
+        RowMasks m0, m1;
+        if (mine > 0) fold(0, s0, u0, m0);
+        for (int n = 0; n < mine && ok; n += 2) {
+            if (n + 1 < mine) fold(n + 1, s1, u1, m1);
+            if (ok) finish(n, s0, u0, m0);
+            if (!ok || n + 1 >= mine) break;
+            if (n + 2 < mine) fold(n + 2, s0, u0, m0);
+            if (ok) finish(n + 1, s1, u1, m1);
         }
-        __syncthreads();  // the stage is read
-        if (threadIdx.x == 0 && k + 2 * p.P < p.tiles) load(k + 2 * p.P, s);
+        copy_empty(p.starts, p.T, p.n_seq, p.D, p.dh_last, p.dh0);
     }
     if (!ok) let_copies_land();
     // this CTA's part of the rates' gradients, the warps in order
     __syncthreads();
-    sh.enter[w][lane] = ds;
+    if (w < kGWarps) sh.enter[0][w][lane] = ds;
     __syncthreads();
     if (w == 0 && in) {
-        float2 v = sh.enter[0][lane];
+        float2 v = sh.enter[0][0][lane];
 #pragma unroll
-        for (int i = 1; i < kGWarps; ++i) {
-            v.x += sh.enter[i][lane].x;
-            v.y += sh.enter[i][lane].y;
-        }
+        for (int i = 1; i < kGWarps; ++i) v = __fadd2_rn(v, sh.enter[0][i][lane]);
         *reinterpret_cast<float2*>(p.part + (long long)turn * p.D + d) = v;
     }
 }
@@ -542,9 +667,12 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const UT* __restrict__ u,
     F4 y = {{0.f, 0.f, 0.f, 0.f}};
     if (prev) y = load4(prev + b * D + d);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const GlrStep k = glr_gates(r.v[j], g.v[j], s.v[j]);
-        y.v[j] = fmaf(k.a, y.v[j], sqrt_approx(k.q) * k.si * x.v[j]);
+    for (int j = 0; j < 4; j += 2) {
+        float2 ka, kb;
+        glr_row<false>(make_float2(r.v[j], r.v[j + 1]), make_float2(g.v[j], g.v[j + 1]), make_float2(x.v[j], x.v[j + 1]),
+                       make_float2(s.v[j], s.v[j + 1]), ka, kb);
+        y.v[j] = fmaf(ka.x, y.v[j], kb.x);
+        y.v[j + 1] = fmaf(ka.y, y.v[j + 1], kb.y);
     }
     store4(next + b * D + d, y.v);
 }

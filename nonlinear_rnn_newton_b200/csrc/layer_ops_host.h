@@ -82,11 +82,11 @@ pararnn_status check_starts(const void* starts)
     return PARARNN_OK;
 }
 
-// header | flags [tiles][S] | maps [tiles][S][32] (16 bytes each) | parts of
-// the rates' gradients [P][D]; the leading two are zeroed before each launch
-// where CTAs share a slab.
+// header | maps [tiles][S][32] (16 bytes each) | parts of the rates' gradients
+// [P][D].  Where CTAs share a slab the header is zeroed and the maps are set to
+// ones before each launch.
 struct GlrLayout {
-    size_t flags, maps, part, total;
+    size_t maps, part, total;
     int S, tiles;
 };
 
@@ -95,8 +95,7 @@ GlrLayout glr_layout(long long T, long long D, int tile)
     GlrLayout ly;
     ly.S = int((D + kGD - 1) / kGD);
     ly.tiles = int((T + tile - 1) / tile);
-    ly.flags = sizeof(WsHeader);
-    ly.maps = align256(ly.flags + size_t(ly.tiles) * ly.S * 4);
+    ly.maps = sizeof(WsHeader);
     ly.part = ly.maps + size_t(ly.tiles) * ly.S * 512;
     ly.total = align256(ly.part + size_t(kGMaxP) * D * 4);
     return ly;
@@ -147,13 +146,13 @@ pararnn_status launch_glr(K kern, int threads, size_t smem, const GlrLayout& ly,
     p->tiles = ly.tiles;
     p->P = std::max(1, std::min({occ * sms / ly.S, ly.tiles, kGMaxP}));
     p->hdr = reinterpret_cast<WsHeader*>(base);
-    p->flags = reinterpret_cast<unsigned*>(base + ly.flags);
-    p->maps = reinterpret_cast<float4*>(base + ly.maps);
+    p->maps = reinterpret_cast<uint4*>(base + ly.maps);
     p->part = reinterpret_cast<float*>(base + ly.part);
     p->wait_ns = kWaitLimitNs;
     const dim3 grid(unsigned(ly.S) * p->P);
     if (p->P > 1) {
         CUDA_TRY(cudaMemsetAsync(ws, 0, ly.maps, st));
+        CUDA_TRY(cudaMemsetAsync(base + ly.maps, 0xff, ly.part - ly.maps, st));
         CUDA_TRY(cudaLaunchCooperativeKernel(f, grid, dim3(threads), args, smem, st));
     } else {
         CUDA_TRY(cudaLaunchKernel(f, grid, dim3(threads), args, smem, st));
