@@ -26,28 +26,29 @@ namespace pararnn {
 // exactly 0, so a gate at the type's lowest value (or -inf) is shut and not
 // nearly shut.
 //
-// p = 1 - e^-l for l >= 0: below 1/4 from its series up to l^6 (the first term
-// left out is l^7/5040, 5e-8 of the value), since 1 - ex2.approx would keep
+// p = 1 - e^-l for l >= 0: below 1/8 from its series up to l^5 (the first term
+// left out is l^6/720, 4e-8 of the value), since 1 - ex2.approx would keep
 // only the bits of e^-l below 1: at l = 1e-3, a common decay, four digits.
 // Pairs of neighbouring channels: the packed fp32 instructions of this
 // architecture take both at once.
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 neg(float2 x) { return make_float2(-x.x, -x.y); }
 
-// Near: every rate of the warp is below 1/4, so l <= rate is too and the far
-// branch (with its special-function use) is left out.
+// a - 1 = -p from nl = -l.  Near: every rate of the warp is below 1/8, so l <=
+// rate is too and the far branch (with its special-function use) is left out.
+// Loops over rows are built for both: a branch in each row would keep the rows'
+// arithmetic from overlapping.
 template <bool Near>
-__device__ __forceinline__ float2 one_minus_exp(float2 l)
+__device__ __forceinline__ float2 exp_minus_one(float2 nl)
 {
-    float2 t = __ffma2_rn(l, both(-1.0f / 720), both(1.0f / 120));
-    t = __ffma2_rn(l, t, both(-1.0f / 24));
-    t = __ffma2_rn(l, t, both(1.0f / 6));
-    t = __ffma2_rn(l, t, both(-0.5f));
-    t = __ffma2_rn(l, t, both(1.0f));
-    t = __fmul2_rn(l, t);
+    float2 t = __ffma2_rn(nl, both(1.0f / 120), both(1.0f / 24));
+    t = __ffma2_rn(nl, t, both(1.0f / 6));
+    t = __ffma2_rn(nl, t, both(0.5f));
+    t = __ffma2_rn(nl, t, both(1.0f));
+    t = __fmul2_rn(nl, t);
     if constexpr (!Near) {
-        const float fx = 1.0f - ex2_approx(-kLog2e * l.x), fy = 1.0f - ex2_approx(-kLog2e * l.y);
-        t = make_float2(l.x < 0.25f ? t.x : fx, l.y < 0.25f ? t.y : fy);
+        const float fx = ex2_approx(kLog2e * nl.x) - 1.0f, fy = ex2_approx(kLog2e * nl.y) - 1.0f;
+        t = make_float2(nl.x > -0.125f ? t.x : fx, nl.y > -0.125f ? t.y : fy);
     }
     return t;
 }
@@ -73,29 +74,30 @@ __device__ __forceinline__ float rsqrt_approx(float x)
     return r;
 }
 
-// l = s sr, a = e^-l, q = 1 - a^2
+// -l = -s sr, a = e^-l, nq = a^2 - 1
 struct Decay2 {
-    float2 l, a, q;
+    float2 nl, a, nq;
 };
 
+// nrate: the rates' negatives
 template <bool Near>
-__device__ __forceinline__ Decay2 glr_decay(float2 sr, float2 rate)
+__device__ __forceinline__ Decay2 glr_decay(float2 sr, float2 nrate)
 {
     Decay2 g;
-    g.l = __fmul2_rn(rate, sr);
-    const float2 p = one_minus_exp<Near>(g.l);
-    g.a = __fadd2_rn(both(1.0f), neg(p));
-    g.q = __fmul2_rn(p, __fadd2_rn(both(2.0f), neg(p)));
+    g.nl = __fmul2_rn(nrate, sr);
+    const float2 np = exp_minus_one<Near>(g.nl);
+    g.a = __fadd2_rn(np, both(1.0f));
+    g.nq = __fmul2_rn(np, __fadd2_rn(np, both(2.0f)));
     return g;
 }
 
 // a and b = m s(i) x of one row
 template <bool Near>
-__device__ __forceinline__ void glr_row(float2 r, float2 i, float2 x, float2 rate, float2& a, float2& b)
+__device__ __forceinline__ void glr_row(float2 r, float2 i, float2 x, float2 nrate, float2& a, float2& b)
 {
-    const Decay2 g = glr_decay<Near>(logistic(r), rate);
+    const Decay2 g = glr_decay<Near>(logistic(r), nrate);
     a = g.a;
-    b = __fmul2_rn(__fmul2_rn(make_float2(sqrt_approx(g.q.x), sqrt_approx(g.q.y)), logistic(i)), x);
+    b = __fmul2_rn(__fmul2_rn(make_float2(sqrt_approx(-g.nq.x), sqrt_approx(-g.nq.y)), logistic(i)), x);
 }
 
 // ------------------------------------------------- sequences in packed rows
@@ -131,15 +133,19 @@ __device__ __forceinline__ RowSeq row_seq(const int* starts, int T, int n_seq, i
     return r;
 }
 
+constexpr int kGD = 64;        // channels of a slab
+constexpr int kGMaxP = 33;     // most CTAs of a slab
+
 // Sequences without rows: `out` gets `in` (or zeros).  The CTAs of the grid
-// share them; called by a CTA's first 256 threads.
+// share them; called by a CTA's computing threads.
+template <int W>
 __device__ __forceinline__ void copy_empty(const int* starts, int T, int n_seq, long long D, const float* in, float* out)
 {
     if (!starts || !out) return;
     for (int s = blockIdx.x; s < n_seq; s += gridDim.x) {
         const int lo = min(max(__ldg(starts + s), 0), T);
         if (min(max(__ldg(starts + s + 1), lo), T) > lo) continue;
-        for (long long d = threadIdx.x; d < D; d += 256) out[s * D + d] = in ? in[s * D + d] : 0.f;
+        for (long long d = threadIdx.x; d < D; d += 32 * W) out[s * D + d] = in ? in[s * D + d] : 0.f;
     }
 }
 
@@ -158,23 +164,27 @@ __device__ __forceinline__ void copy_empty(const int* starts, int T, int n_seq, 
 // tile ended with: no chain of CTAs waiting for one another's states, and a
 // fixed order of operations (the same bits every run).
 //
-// Warps 0..7 of a CTA compute: warp w takes rows w kRows .. of a tile, lane l
-// channels 2 l and 2 l + 1.  They fold tile n + 1 before they run through tile
-// n, so that the way of a map to the other CTAs and of theirs to here (two
-// trips to L2, more than a microsecond) passes behind a tile's work.  Warp 8
-// loads the tiles (four stages, TMA), joins the warps' maps, publishes, looks
-// up the others' and hands each warp the state entering its rows.
+// Ten warps of a CTA compute: warp w takes rows w kRows .. of a tile, lane l
+// channels 2 l and 2 l + 1.  They fold one tile (scan) or two (adjoint) ahead
+// of the tile that they run through, so that the way of a map to the other CTAs
+// and of theirs to here, about 2 us under load, passes behind their work.  Two
+// more warps take the tiles in turn: they load them (TMA), join the warps'
+// maps, publish, look up the others' and hand each warp the state entering its
+// rows; with one such warp its own trips to L2 set the pace (adjoint B4 L16384
+// D2048: 0.83 against 0.60 ms).
+//
+// The scan keeps a and b of the folded rows in registers (12 rows a warp, 4
+// registers each, twice) and so gives a stage back at once; the adjoint keeps
+// s(r) and the upstream gradients and reads the rest again.  Measured at B1
+// L65536 D2048, bf16, scan: 12 rows a warp and one tile ahead 0.311 ms; 6 rows
+// and two ahead 0.331; 14 warps of 9 rows 0.364; b kept in the stages' place
+// instead 0.332.  With every channel slab a CTA's own (no maps to wait for) a
+// scan runs at 5.3 TB/s, and the adjoint at 6.3.
 //
 // A published map needs no flag: the maps' memory starts as words of all ones,
 // a written word is never that, and a reader takes a map when none of its
 // words is.  The sign of A (a product of decays, not negative) says whether
 // the tile holds a cut.
-
-constexpr int kGD = 64;        // channels of a slab
-constexpr int kGWarps = 8;     // that compute
-constexpr int kGThreads = 32 * (kGWarps + 1);
-constexpr int kGStages = 4;
-constexpr int kGMaxP = 33;     // most CTAs of a slab
 
 struct GlrParams {
     const float *rate, *h0;
@@ -201,23 +211,29 @@ __device__ __forceinline__ float2 apply(const Map2& m, float2 y)
 }
 
 // The shared parts of both scans' shared memory behind the stages.
+constexpr int kGMaxStages = 5;
+template <int W, int NS>  // computing warps, folded tiles at a time
 struct GlrShared {
-    float4 agg[2][kGWarps][32];   // the warps' maps, by the tile's parity
-    float2 enter[2][kGWarps][32]; // the state entering each warp's rows
-    int cut[2][kGWarps];
-    uint64_t full[kGStages], empty[kGStages];
-    uint64_t agg_full[2], entered[2];
+    static constexpr int kSets = NS;
+    float4 agg[NS][W][32];  // the warps' maps of the CTA's tile n, at n % NS
+    float2 enter[2][W][32]; // the state entering each warp's rows, at n % 2
+    int cut[NS][W];
+    uint64_t full[kGMaxStages], empty[kGMaxStages];
+    float2 own[2][32];            // the state that tile n ended with, at n % 2
+    uint64_t agg_full[NS], entered[2], passed[2];
 };
 
-__device__ __forceinline__ void glr_init(GlrShared& sh)
+template <int W, int NS>
+__device__ __forceinline__ void glr_init(GlrShared<W, NS>& sh)
 {
-    for (int i = 0; i < kGStages; ++i) {
+    for (int i = 0; i < kGMaxStages; ++i) {
         mbar_init(&sh.full[i], 1);
-        mbar_init(&sh.empty[i], kGWarps);
+        mbar_init(&sh.empty[i], W);
     }
+    for (int i = 0; i < NS; ++i) mbar_init(&sh.agg_full[i], W);
     for (int i = 0; i < 2; ++i) {
-        mbar_init(&sh.agg_full[i], kGWarps);
         mbar_init(&sh.entered[i], 1);
+        mbar_init(&sh.passed[i], 1);
     }
     fence_mbar_init();
 }
@@ -232,81 +248,99 @@ __device__ __forceinline__ unsigned map_word(float x)
 __device__ __forceinline__ uint4 ld_map(const uint4* p)
 {
     uint4 v;
-    asm volatile("ld.volatile.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.relaxed.gpu.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p)
                  : "memory");
     return v;
 }
 
-// The control warp, with the warps' maps of tile k (the CTA's n-th) in shared
-// memory: publishes the tile's map, finds the state entering the tile (`own`
-// is the state the CTA's last tile ended with; it becomes this one's) and from
-// it the state entering each warp's rows.  False when a wait ran out.
-template <bool Reverse>
-__device__ __forceinline__ bool glr_carry(const GlrParams& p, GlrShared& sh, int slab, int k, int n, int lane, float2& own)
+template <bool Reverse, int W, int NS>
+__device__ __forceinline__ Map2 warp_map(const GlrShared<W, NS>& sh, int n, int i, int lane)
 {
-    auto warp_at = [](int i) { return Reverse ? kGWarps - 1 - i : i; };
-    const int par = n & 1;
-    Map2 m[kGWarps];
+    const int w = Reverse ? W - 1 - i : i;  // the warp that comes i-th
+    const float4 v = sh.agg[n % NS][w][lane];
+    return Map2{make_float2(v.x, v.z), make_float2(v.y, v.w), sh.cut[n % NS][w] != 0};
+}
+
+// The control warp, with the warps' maps of tile k (the CTA's n-th) in shared
+// memory: joins them and publishes the tile's map.
+template <bool Reverse, int W, int NS>
+__device__ __forceinline__ void glr_publish(const GlrParams& p, const GlrShared<W, NS>& sh, int slab, int k, int n, int lane)
+{
+    Map2 all = warp_map<Reverse>(sh, n, 0, lane);
 #pragma unroll
-    for (int i = 0; i < kGWarps; ++i) {
-        const float4 v = sh.agg[par][warp_at(i)][lane];
-        m[i] = Map2{make_float2(v.x, v.z), make_float2(v.y, v.w), sh.cut[par][warp_at(i)] != 0};
+    for (int i = 1; i < W; ++i) {
+        const Map2 m = warp_map<Reverse>(sh, n, i, lane);
+        all.b = apply(m, all.b);
+        all.a = __fmul2_rn(m.a, all.a);
+        all.cut |= m.cut;
     }
-    if (p.P > 1) {
-        Map2 all = m[0];
+    uint4 out = make_uint4(map_word(all.a.x), map_word(all.b.x), map_word(all.a.y), map_word(all.b.y));
+    out.x = all.cut ? out.x | 0x80000000u : out.x & 0x7fffffffu;
+    asm volatile("st.relaxed.gpu.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p.maps + (size_t(k) * p.S + slab) * 32 + lane),
+                 "r"(out.x), "r"(out.y), "r"(out.z), "r"(out.w)
+                 : "memory");
+}
+
+// Then the state entering tile k, from the one the CTA's tile before ended with
+// (the other control warp passes it on), and from it the state entering each
+// warp's rows.  False when a wait ran out.
+template <bool Reverse, int W, int NS>
+__device__ __forceinline__ bool glr_carry(const GlrParams& p, GlrShared<W, NS>& sh, int slab, int k, int n, int lane)
+{
+    // the tiles since this CTA's last one (all of them in its first turn)
+    const int first = max(k - p.P + 1, 0), cnt = p.P > 1 ? k - first : 0;
+    const uint4* from = p.maps + (size_t(first) * p.S + slab) * 32 + lane;
+    Map2 all{both(1.f), both(0.f), false};
+    for (int i = 0; i < cnt; i += 8) {
+        uint4 v[8];
+        long long t0 = 0;
+        for (;;) {
+            bool there = true;
 #pragma unroll
-        for (int i = 1; i < kGWarps; ++i) {
-            all.b = apply(m[i], all.b);
-            all.a = __fmul2_rn(m[i].a, all.a);
-            all.cut |= m[i].cut;
-        }
-        uint4 out = make_uint4(map_word(all.a.x), map_word(all.b.x), map_word(all.a.y), map_word(all.b.y));
-        out.x = all.cut ? out.x | 0x80000000u : out.x & 0x7fffffffu;
-        uint4* to = p.maps + (size_t(k) * p.S + slab) * 32 + lane;
-        asm volatile("st.volatile.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(to), "r"(out.x), "r"(out.y), "r"(out.z),
-                     "r"(out.w)
-                     : "memory");
-        // the tiles since this CTA's last one (all of them in its first turn)
-        const int first = max(k - p.P + 1, 0), cnt = k - first;
-        const uint4* from = p.maps + (size_t(first) * p.S + slab) * 32 + lane;
-        for (int i = 0; i < cnt; i += 8) {
-            uint4 v[8];
-            long long t0 = 0;
-            for (;;) {
-                bool there = true;
+            for (int j = 0; j < 8; ++j) v[j] = i + j < cnt ? ld_map(from + size_t(i + j) * p.S * 32) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = i + j < cnt ? ld_map(from + size_t(i + j) * p.S * 32) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    there = there && v[j].x != ~0u && v[j].y != ~0u && v[j].z != ~0u && v[j].w != ~0u;
-                if (__all_sync(0xffffffffu, there)) break;
-                if (t0 == 0) t0 = clock64();
-                const bool late = clock64() - t0 > (long long)(2 * p.wait_ns);
-                if (__any_sync(0xffffffffu, late || error_raised(&p.hdr->error))) {
-                    raise_error(&p.hdr->error, PARARNN_ERR_TIMEOUT);
-                    return false;
-                }
+            for (int j = 0; j < 8; ++j)
+                there = there && v[j].x != ~0u && v[j].y != ~0u && v[j].z != ~0u && v[j].w != ~0u;
+            if (__all_sync(0xffffffffu, there)) break;
+            if (t0 == 0) t0 = clock64();
+            const bool late = clock64() - t0 > (long long)(2 * p.wait_ns);
+            if (__any_sync(0xffffffffu, late)) {
+                raise_error(&p.hdr->error, PARARNN_ERR_TIMEOUT);
+                return false;
             }
+        }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (i + j < cnt) {
-                    const bool cut = v[j].x >> 31;
-                    own = apply(Map2{make_float2(__uint_as_float(v[j].x & 0x7fffffffu), __uint_as_float(v[j].z)),
-                                     make_float2(__uint_as_float(v[j].y), __uint_as_float(v[j].w)), cut},
-                                own);
-                }
+        for (int j = 0; j < 8; ++j) {
+            if (i + j < cnt) {
+                const Map2 m{make_float2(__uint_as_float(v[j].x & 0x7fffffffu), __uint_as_float(v[j].z)),
+                             make_float2(__uint_as_float(v[j].y), __uint_as_float(v[j].w)), (v[j].x >> 31) != 0};
+                all.b = apply(m, all.b);
+                all.a = __fmul2_rn(m.a, all.a);
+                all.cut |= m.cut;
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < kGWarps; ++i) {
-        sh.enter[par][warp_at(i)][lane] = own;
-        own = apply(m[i], own);
+    float2 own = both(0.f);
+    if (n > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait_clocked(&sh.passed[(n - 1) & 1], uint32_t((n - 1) >> 1) & 1u, &p.hdr->error,
+                                                       p.wait_ns)))
+            return false;
+        own = sh.own[(n - 1) & 1][lane];
     }
+    if (cnt) own = apply(all, own);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        sh.enter[n & 1][Reverse ? W - 1 - i : i][lane] = own;
+        own = apply(warp_map<Reverse>(sh, n, i, lane), own);
+    }
+    sh.own[n & 1][lane] = own;
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.entered[par]);
+    if (lane == 0) {
+        mbar_arrive(&sh.passed[n & 1]);
+        mbar_arrive(&sh.entered[n & 1]);
+    }
     return true;
 }
 
@@ -321,36 +355,56 @@ __device__ __forceinline__ float2 pair_of(const UT* p)
 struct RowMasks {
     unsigned firsts, lasts, mine;
     int owner;
+    // rows within one sequence, none its first or last
+    __device__ __forceinline__ bool plain() const { return (firsts | lasts | ~mine) == 0; }
 };
 
-__device__ __forceinline__ RowMasks row_masks(const GlrParams& p, int t0, int rows, int lane)
+// The rows strictly inside the sequence that a warp met last: tiles within them
+// need no look at the sequences.
+struct PlainRows {
+    int lo = 0, hi = 0;  // first row behind the sequence's first, its last row
+};
+
+__device__ __forceinline__ RowMasks row_masks(const GlrParams& p, int t0, int rows, int lane, PlainRows& plain)
 {
+    RowMasks m{0u, 0u, ~0u, 0};
+    if (t0 >= plain.lo && t0 + rows <= plain.hi) return m;
     const RowSeq rs = row_seq(p.starts, p.T, p.n_seq, p.L, lane < rows ? t0 + lane : -1);
-    RowMasks m;
     m.firsts = __ballot_sync(0xffffffffu, rs.first);
     m.lasts = __ballot_sync(0xffffffffu, rs.last);
-    m.mine = __ballot_sync(0xffffffffu, rs.owner >= 0);
+    m.mine = __ballot_sync(0xffffffffu, rs.owner >= 0) | (~0u << rows);
     m.owner = rs.owner;
+    // the sequence of the last row of any
+    const unsigned any = m.mine & ((1u << rows) - 1u);
+    if (any) {
+        const int o = __shfl_sync(0xffffffffu, rs.owner, 31 - __clz(any));
+        plain.lo = (p.starts ? max(__ldg(p.starts + o), 0) : o * p.L) + 1;
+        plain.hi = (p.starts ? min(__ldg(p.starts + o + 1), p.T) : (o + 1) * p.L) - 1;
+    }
     return m;
 }
 
 template <class UT>
 struct GlrScanLayout {
-    static constexpr int kRows = sizeof(UT) == 2 ? 12 : 8;  // of a warp
-    static constexpr int kTile = kRows * kGWarps;
+    static constexpr int kWarps = 10;  // that compute; two more control
+    static constexpr int kThreads = 32 * (kWarps + 2);
+    static constexpr int kAhead = 1, kSets = kAhead + 1;  // tiles folded ahead of the one run through
+    static constexpr int kRows = sizeof(UT) == 2 ? 12 : 6;  // of a warp
+    static constexpr int kStages = 4;
+    static constexpr int kTile = kRows * kWarps;
     static constexpr size_t stage_bytes = size_t(kTile) * 3 * kGD * sizeof(UT);
-    static constexpr size_t smem_bytes = kGStages * stage_bytes + sizeof(GlrShared) + 128;
+    static constexpr size_t smem_bytes = kStages * stage_bytes + sizeof(GlrShared<kWarps, kSets>) + 128;
     static_assert(smem_bytes <= 232448, "shared memory");
 };
 
 template <class UT>
-__global__ void __launch_bounds__(kGThreads, 1) glr_scan_kernel(const __grid_constant__ CUtensorMap tm_u, const GlrParams p)
+__global__ void __launch_bounds__(GlrScanLayout<UT>::kThreads, 1) glr_scan_kernel(const __grid_constant__ CUtensorMap tm_u, const GlrParams p)
 {
     using LY = GlrScanLayout<UT>;
-    constexpr int R = LY::kRows;
+    constexpr int R = LY::kRows, W = LY::kWarps, NS = LY::kSets, A_ = LY::kAhead;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
-    GlrShared& sh = *reinterpret_cast<GlrShared*>(smem + kGStages * LY::stage_bytes);
+    GlrShared<W, NS>& sh = *reinterpret_cast<GlrShared<W, NS>*>(smem + LY::kStages * LY::stage_bytes);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slab = blockIdx.x % p.S, turn = blockIdx.x / p.S;
     const int d = slab * kGD + 2 * lane;
@@ -358,40 +412,42 @@ __global__ void __launch_bounds__(kGThreads, 1) glr_scan_kernel(const __grid_con
     const int mine = turn < p.tiles ? (p.tiles - 1 - turn) / p.P + 1 : 0;  // tiles turn, turn + P, ..
     int* err = &p.hdr->error;
     if (threadIdx.x == 0) {
-        if (p.P == 1 && blockIdx.x == 0) clear_outcome(p.hdr);
+        if (blockIdx.x == 0) clear_outcome(p.hdr);
         glr_init(sh);
     }
     __syncthreads();
     bool ok = true;
-    if (w == kGWarps) {
+    if (w >= W) {
         auto load = [&](int n) {
-            const int s = n % kGStages;
+            const int s = n % LY::kStages;
             mbar_arrive_expect_tx(&sh.full[s], uint32_t(LY::stage_bytes));
             tma_load_3d(smem + s * LY::stage_bytes, &tm_u, slab * kGD, 0, (turn + n * p.P) * LY::kTile, &sh.full[s]);
         };
-        if (lane == 0)
-            for (int n = 0; n < min(mine, kGStages); ++n) load(n);
-        float2 own = make_float2(0.f, 0.f);
-        for (int n = 0; n < mine && ok; ++n) {
-            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.agg_full[n & 1], uint32_t(n >> 1) & 1u, err, p.wait_ns));
+        if (w == W && lane == 0)
+            for (int n = 0; n < min(mine, LY::kStages); ++n) load(n);
+        // the two control warps take the tiles in turn
+        for (int n = w - W; n < mine && ok; n += 2) {
+            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.agg_full[n % NS], uint32_t(n / NS) & 1u, err, p.wait_ns));
             if (!ok) break;
-            if (lane == 0 && n + kGStages < mine) load(n + kGStages);  // every warp has read the stage
-            ok = glr_carry<false>(p, sh, slab, turn + n * p.P, n, lane, own);
+            if (p.P > 1) glr_publish<false>(p, sh, slab, turn + n * p.P, n, lane);
+            if (lane == 0 && n + LY::kStages < mine) load(n + LY::kStages);  // every warp has read the stage
+            ok = glr_carry<false>(p, sh, slab, turn + n * p.P, n, lane);
         }
     } else {
-        const float2 rate = in ? pair_of(p.rate + d) : make_float2(0.f, 0.f);
-        const bool near = __all_sync(0xffffffffu, rate.x < 0.25f && rate.y < 0.25f);
+        const float2 nrate = in ? neg(pair_of(p.rate + d)) : both(0.f);
+        const bool near = __all_sync(0xffffffffu, nrate.x > -0.125f && nrate.y > -0.125f);
+        PlainRows plain;
         // fold tile n: its rows' a and b into registers, the warp's map out
         auto fold = [&](int n, float2(&a)[R], float2(&b)[R], RowMasks& rm) {
-            const int s = n % kGStages;
-            rm = row_masks(p, (turn + n * p.P) * LY::kTile + w * R, R, lane);
-            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.full[s], uint32_t(n / kGStages) & 1u, err, p.wait_ns));
+            const int s = n % LY::kStages;
+            rm = row_masks(p, (turn + n * p.P) * LY::kTile + w * R, R, lane, plain);
+            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.full[s], uint32_t(n / LY::kStages) & 1u, err, p.wait_ns));
             const UT* src = reinterpret_cast<const UT*>(smem + s * LY::stage_bytes) + size_t(w) * R * 3 * kGD + 2 * lane;
             auto rows = [&](auto is_near) {
 #pragma unroll
                 for (int i = 0; i < R; ++i)
                     glr_row<decltype(is_near)::value>(pair_of(src + i * 3 * kGD), pair_of(src + (i * 3 + 1) * kGD),
-                                                      pair_of(src + (i * 3 + 2) * kGD), rate, a[i], b[i]);
+                                                      pair_of(src + (i * 3 + 2) * kGD), nrate, a[i], b[i]);
             };
             if (near) rows(std::true_type());
             else rows(std::false_type());
@@ -402,7 +458,7 @@ __global__ void __launch_bounds__(kGThreads, 1) glr_scan_kernel(const __grid_con
                     B = __ffma2_rn(a[i], B, b[i]);
                     A = __fmul2_rn(A, a[i]);
                 }
-            } else {
+            } else {  // the states before the sequences that start here; what came before is cut
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     const bool cut = (rm.firsts >> i) & 1u;
@@ -412,10 +468,10 @@ __global__ void __launch_bounds__(kGThreads, 1) glr_scan_kernel(const __grid_con
                     A = __fmul2_rn(A, a[i]);
                 }
             }
-            sh.agg[n & 1][w][lane] = make_float4(A.x, B.x, A.y, B.y);
-            if (lane == 0) sh.cut[n & 1][w] = rm.firsts != 0;
+            sh.agg[n % NS][w][lane] = make_float4(A.x, B.x, A.y, B.y);
+            if (lane == 0) sh.cut[n % NS][w] = rm.firsts != 0;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.agg_full[n & 1]);
+            if (lane == 0) mbar_arrive(&sh.agg_full[n % NS]);
         };
         // run through tile n from the state entering this warp's rows
         auto finish = [&](int n, const float2(&a)[R], const float2(&b)[R], const RowMasks& rm) {
@@ -424,7 +480,7 @@ __global__ void __launch_bounds__(kGThreads, 1) glr_scan_kernel(const __grid_con
             const int t0 = (turn + n * p.P) * LY::kTile + w * R;
             float2 y = sh.enter[n & 1][w][lane];
             float* h = p.h + (long long)t0 * p.D + d;
-            if (rm.firsts == 0 && rm.lasts == 0 && rm.mine == (1u << R) - 1u) {
+            if (rm.plain()) {
 #pragma unroll
                 for (int i = 0; i < R; ++i) {
                     y = __ffma2_rn(a[i], y, b[i]);
@@ -436,35 +492,42 @@ __global__ void __launch_bounds__(kGThreads, 1) glr_scan_kernel(const __grid_con
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 y = apply(Map2{a[i], b[i], ((rm.firsts >> i) & 1u) != 0}, y);
-                if (in && ((rm.mine >> i) & 1u)) *reinterpret_cast<float2*>(h + i * p.D) = y;
+                if (in && ((rm.mine >> i) & 1u)) *reinterpret_cast<float2*>(h) = y;
+                h += p.D;
                 if ((rm.lasts >> i) & 1u) {
                     const long long o = __shfl_sync(0xffffffffu, rm.owner, i);
                     if (p.h_last && in) *reinterpret_cast<float2*>(p.h_last + o * p.D + d) = y;
                 }
             }
         };
-        float2 a0[R], b0[R], a1[R], b1[R];
-        RowMasks m0, m1;
-        if (mine > 0) fold(0, a0, b0, m0);
-        for (int n = 0; n < mine && ok; n += 2) {
-            if (n + 1 < mine) fold(n + 1, a1, b1, m1);
-            if (ok) finish(n, a0, b0, m0);
-            if (!ok || n + 1 >= mine) break;
-            if (n + 2 < mine) fold(n + 2, a0, b0, m0);
-            if (ok) finish(n + 1, a1, b1, m1);
+        float2 a[NS][R], b[NS][R];
+        RowMasks rm[NS];
+        if (mine > 0) fold(0, a[0], b[0], rm[0]);
+        if (A_ > 1 && mine > 1) fold(1, a[1], b[1], rm[1]);
+        for (int n = 0; n < mine && ok; n += NS) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                if (n + i >= mine || !ok) break;
+                if (n + i + A_ < mine) fold(n + i + A_, a[(i + A_) % NS], b[(i + A_) % NS], rm[(i + A_) % NS]);
+                if (ok) finish(n + i, a[i], b[i], rm[i]);
+            }
         }
-        copy_empty(p.starts, p.T, p.n_seq, p.D, p.h0, p.h_last);
+        copy_empty<W>(p.starts, p.T, p.n_seq, p.D, p.h0, p.h_last);
     }
     if (!ok) let_copies_land();
 }
 
 template <class UT>
 struct GlrAdjointLayout {
-    static constexpr int kRows = sizeof(UT) == 2 ? 7 : 5;  // of a warp
-    static constexpr int kTile = kRows * kGWarps;
+    static constexpr int kWarps = 10;  // that compute; two more control
+    static constexpr int kThreads = 32 * (kWarps + 2);
+    static constexpr int kAhead = 2, kSets = kAhead + 1;  // tiles folded ahead of the one run through
+    static constexpr int kRows = sizeof(UT) == 2 ? 4 : 3;  // of a warp
+    static constexpr int kStages = 5;
+    static constexpr int kTile = kRows * kWarps;
     static constexpr size_t u_bytes = size_t(kTile) * 3 * kGD * sizeof(UT), f_bytes = size_t(kTile) * kGD * 4;
     static constexpr size_t stage_bytes = u_bytes + 2 * f_bytes;
-    static constexpr size_t smem_bytes = kGStages * stage_bytes + sizeof(GlrShared) + 128;
+    static constexpr size_t smem_bytes = kStages * stage_bytes + sizeof(GlrShared<kWarps, kSets>) + 128;
     static_assert(smem_bytes <= 232448, "shared memory");
 };
 
@@ -473,15 +536,15 @@ struct GlrAdjointLayout {
 // start before row 0, where there is nothing).  A stage stays until its tile
 // has been run through.
 template <class UT>
-__global__ void __launch_bounds__(kGThreads, 1)
+__global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
     glr_adjoint_kernel(const __grid_constant__ CUtensorMap tm_u, const __grid_constant__ CUtensorMap tm_h,
                        const __grid_constant__ CUtensorMap tm_dh, const GlrParams p)
 {
     using LY = GlrAdjointLayout<UT>;
-    constexpr int R = LY::kRows;
+    constexpr int R = LY::kRows, W = LY::kWarps, NS = LY::kSets, A_ = LY::kAhead;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
-    GlrShared& sh = *reinterpret_cast<GlrShared*>(smem + kGStages * LY::stage_bytes);
+    GlrShared<W, NS>& sh = *reinterpret_cast<GlrShared<W, NS>*>(smem + LY::kStages * LY::stage_bytes);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slab = blockIdx.x % p.S, turn = blockIdx.x / p.S;
     const int d = slab * kGD + 2 * lane;
@@ -489,43 +552,46 @@ __global__ void __launch_bounds__(kGThreads, 1)
     const int mine = turn < p.tiles ? (p.tiles - 1 - turn) / p.P + 1 : 0;
     int* err = &p.hdr->error;
     if (threadIdx.x == 0) {
-        if (p.P == 1 && blockIdx.x == 0) clear_outcome(p.hdr);
+        if (blockIdx.x == 0) clear_outcome(p.hdr);
         glr_init(sh);
     }
     __syncthreads();
     bool ok = true;
-    float2 ds = make_float2(0.f, 0.f);
-    if (w == kGWarps) {
+    float2 nds = both(0.f);  // minus the rates' gradients
+    if (w >= W) {
         auto load = [&](int n) {
-            const int s = n % kGStages, t = p.T - (turn + n * p.P + 1) * LY::kTile;
+            const int s = n % LY::kStages, t = p.T - (turn + n * p.P + 1) * LY::kTile;
             unsigned char* to = smem + s * LY::stage_bytes;
             mbar_arrive_expect_tx(&sh.full[s], uint32_t(LY::stage_bytes));
             tma_load_3d(to, &tm_u, slab * kGD, 0, t, &sh.full[s]);
             tma_load_2d(to + LY::u_bytes, &tm_h, slab * kGD, t - 1, &sh.full[s]);  // the states before the rows
             tma_load_2d(to + LY::u_bytes + LY::f_bytes, &tm_dh, slab * kGD, t, &sh.full[s]);
         };
-        if (lane == 0)
-            for (int n = 0; n < min(mine, kGStages); ++n) load(n);
-        float2 own = make_float2(0.f, 0.f);
-        for (int n = 0; n < mine && ok; ++n) {
-            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.agg_full[n & 1], uint32_t(n >> 1) & 1u, err, p.wait_ns));
+        if (w == W && lane == 0)
+            for (int n = 0; n < min(mine, LY::kStages); ++n) load(n);
+        // the two control warps take the tiles in turn
+        for (int n = w - W; n < mine && ok; n += 2) {
+            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.agg_full[n % NS], uint32_t(n / NS) & 1u, err, p.wait_ns));
             if (!ok) break;
-            ok = glr_carry<true>(p, sh, slab, turn + n * p.P, n, lane, own);
-            // the warps run through tile n - 1 before they fold tile n + 1
-            if (ok && n > 0 && n - 1 + kGStages < mine) {
-                const int s = (n - 1) % kGStages;
-                ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.empty[s], uint32_t((n - 1) / kGStages) & 1u, err, p.wait_ns));
-                if (ok && lane == 0) load(n - 1 + kGStages);
+            if (p.P > 1) glr_publish<true>(p, sh, slab, turn + n * p.P, n, lane);
+            // the warps run through tile n - kAhead next, and fold tile n + 1 then
+            if (n >= A_ && n - A_ + LY::kStages < mine) {
+                const int s = (n - A_) % LY::kStages;
+                ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.empty[s], uint32_t((n - A_) / LY::kStages) & 1u, err, p.wait_ns));
+                if (!ok) break;
+                if (lane == 0) load(n - A_ + LY::kStages);
             }
+            ok = glr_carry<true>(p, sh, slab, turn + n * p.P, n, lane);
         }
     } else {
-        const float2 rate = in ? pair_of(p.rate + d) : make_float2(0.f, 0.f);
-        const bool near = __all_sync(0xffffffffu, rate.x < 0.25f && rate.y < 0.25f);
+        const float2 nrate = in ? neg(pair_of(p.rate + d)) : both(0.f);
+        const bool near = __all_sync(0xffffffffu, nrate.x > -0.125f && nrate.y > -0.125f);
+        PlainRows plain;
         // G = a (up + G of the row behind): the map of a row is (a, a up)
         auto fold = [&](int n, float2(&sr)[R], float2(&up)[R], RowMasks& rm) {
-            const int s = n % kGStages;
-            rm = row_masks(p, p.T - (turn + n * p.P + 1) * LY::kTile + w * R, R, lane);
-            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.full[s], uint32_t(n / kGStages) & 1u, err, p.wait_ns));
+            const int s = n % LY::kStages;
+            rm = row_masks(p, p.T - (turn + n * p.P + 1) * LY::kTile + w * R, R, lane, plain);
+            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.full[s], uint32_t(n / LY::kStages) & 1u, err, p.wait_ns));
             const unsigned char* stage = smem + s * LY::stage_bytes;
             const UT* su = reinterpret_cast<const UT*>(stage) + size_t(w) * R * 3 * kGD + 2 * lane;
             const float* sd = reinterpret_cast<const float*>(stage + LY::u_bytes + LY::f_bytes) + w * R * kGD + 2 * lane;
@@ -545,7 +611,7 @@ __global__ void __launch_bounds__(kGThreads, 1)
             auto rows = [&](auto is_near) {
 #pragma unroll
                 for (int i = R - 1; i >= 0; --i) {
-                    const float2 a = glr_decay<decltype(is_near)::value>(sr[i], rate).a;
+                    const float2 a = glr_decay<decltype(is_near)::value>(sr[i], nrate).a;
                     const bool cut = (rm.lasts >> i) & 1u;
                     B = __fmul2_rn(a, cut ? up[i] : __fadd2_rn(up[i], B));
                     A = __fmul2_rn(A, a);
@@ -553,81 +619,82 @@ __global__ void __launch_bounds__(kGThreads, 1)
             };
             if (near) rows(std::true_type());
             else rows(std::false_type());
-            sh.agg[n & 1][w][lane] = make_float4(A.x, B.x, A.y, B.y);
-            if (lane == 0) sh.cut[n & 1][w] = rm.lasts != 0;
+            sh.agg[n % NS][w][lane] = make_float4(A.x, B.x, A.y, B.y);
+            if (lane == 0) sh.cut[n % NS][w] = rm.lasts != 0;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.agg_full[n & 1]);
+            if (lane == 0) mbar_arrive(&sh.agg_full[n % NS]);
         };
         auto finish = [&](int n, const float2(&sr)[R], const float2(&up)[R], const RowMasks& rm) {
             ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.entered[n & 1], uint32_t(n >> 1) & 1u, err, p.wait_ns));
             if (!ok) return;
-            const int s = n % kGStages, t0 = p.T - (turn + n * p.P + 1) * LY::kTile + w * R;
+            const int s = n % LY::kStages, t0 = p.T - (turn + n * p.P + 1) * LY::kTile + w * R;
             const unsigned char* stage = smem + s * LY::stage_bytes;
             const UT* su = reinterpret_cast<const UT*>(stage) + size_t(w) * R * 3 * kGD + 2 * lane;
             const float* sb = reinterpret_cast<const float*>(stage + LY::u_bytes) + w * R * kGD + 2 * lane;
             float2 G = sh.enter[n & 1][w][lane];
-            auto rows = [&](auto is_near) {
+            auto run = [&](auto is_near, auto is_plain) {
 #pragma unroll
                 for (int i = R - 1; i >= 0; --i) {
                     const float2 si = logistic(pair_of(su + (i * 3 + 1) * kGD)), x = pair_of(su + (i * 3 + 2) * kGD);
                     float2 before = pair_of(sb + i * kGD);
-                    if ((rm.firsts >> i) & 1u) {
+                    if (!decltype(is_plain)::value && ((rm.firsts >> i) & 1u)) {
                         const long long o = __shfl_sync(0xffffffffu, rm.owner, i);
                         before = p.h0 && in ? pair_of(p.h0 + o * p.D + d) : both(0.f);
                     }
-                    const float2 lam = (rm.lasts >> i) & 1u ? up[i] : __fadd2_rn(up[i], G);
-                    const Decay2 g = glr_decay<decltype(is_near)::value>(sr[i], rate);
+                    const float2 lam = !decltype(is_plain)::value && ((rm.lasts >> i) & 1u) ? up[i] : __fadd2_rn(up[i], G);
+                    const Decay2 g = glr_decay<decltype(is_near)::value>(sr[i], nrate);
                     G = __fmul2_rn(g.a, lam);
-                    if (!((rm.mine >> i) & 1u)) continue;
-                    // 1 / m; where l = 0 (a shut gate) the root has no slope: its terms are 0
-                    const float2 im = make_float2(g.q.x > 1e-37f ? rsqrt_approx(g.q.x) : 0.f,
-                                                  g.q.y > 1e-37f ? rsqrt_approx(g.q.y) : 0.f);
-                    const float2 lsi = __fmul2_rn(lam, si);
-                    const float2 dx = __fmul2_rn(lsi, __fmul2_rn(g.q, im));
-                    const float2 di = __fmul2_rn(__fmul2_rn(dx, x), __fadd2_rn(both(1.f), neg(si)));
-                    // dl = lam (s(i) x a^2 / m - a h)
-                    const float2 in_m = __fmul2_rn(__fmul2_rn(__fmul2_rn(lsi, x), __fmul2_rn(g.a, g.a)), im);
-                    const float2 dl = __ffma2_rn(neg(G), before, in_m);
-                    const float2 dr = __fmul2_rn(__fmul2_rn(dl, g.l), __fadd2_rn(both(1.f), neg(sr[i])));
-                    ds = __ffma2_rn(dl, sr[i], ds);
+                    if (!decltype(is_plain)::value && !((rm.mine >> i) & 1u)) continue;
+                    // -1 / m; where l = 0 (a shut gate) the root has no slope: its terms are 0
+                    const float2 nim = make_float2(g.nq.x < -1e-37f ? -rsqrt_approx(-g.nq.x) : 0.f,
+                                                   g.nq.y < -1e-37f ? -rsqrt_approx(-g.nq.y) : 0.f);
+                    const float2 lsi = __fmul2_rn(lam, si), lx = __fmul2_rn(lsi, x);
+                    const float2 dx = __fmul2_rn(lsi, __fmul2_rn(g.nq, nim));
+                    const float2 di = __fmul2_rn(__fmul2_rn(dx, x), __ffma2_rn(si, both(-1.f), both(1.f)));
+                    // dl = lam (s(i) x a^2 / m - a h), negated
+                    const float2 ndl = __ffma2_rn(G, before, __fmul2_rn(__fmul2_rn(lx, __fmul2_rn(g.a, g.a)), nim));
+                    const float2 dr = __fmul2_rn(__fmul2_rn(ndl, g.nl), __ffma2_rn(sr[i], both(-1.f), both(1.f)));
+                    nds = __ffma2_rn(ndl, sr[i], nds);
                     if (in) {
                         float* q = p.du + (long long)(t0 + i) * 3 * p.D + d;
                         *reinterpret_cast<float2*>(q) = dr;
                         *reinterpret_cast<float2*>(q + p.D) = di;
                         *reinterpret_cast<float2*>(q + 2 * p.D) = dx;
                     }
-                    if ((rm.firsts >> i) & 1u) {
+                    if (!decltype(is_plain)::value && ((rm.firsts >> i) & 1u)) {
                         const long long o = __shfl_sync(0xffffffffu, rm.owner, i);
                         if (p.dh0 && in) *reinterpret_cast<float2*>(p.dh0 + o * p.D + d) = G;
                     }
                 }
             };
-            if (near) rows(std::true_type());
-            else rows(std::false_type());
+            if (near && rm.plain()) run(std::true_type(), std::true_type());
+            else run(std::false_type(), std::false_type());
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.empty[s]);
         };
-        float2 s0[R], u0[R], s1[R], u1[R];
-        RowMasks m0, m1;
-        if (mine > 0) fold(0, s0, u0, m0);
-        for (int n = 0; n < mine && ok; n += 2) {
-            if (n + 1 < mine) fold(n + 1, s1, u1, m1);
-            if (ok) finish(n, s0, u0, m0);
-            if (!ok || n + 1 >= mine) break;
-            if (n + 2 < mine) fold(n + 2, s0, u0, m0);
-            if (ok) finish(n + 1, s1, u1, m1);
+        float2 sr[NS][R], up[NS][R];
+        RowMasks rm[NS];
+        if (mine > 0) fold(0, sr[0], up[0], rm[0]);
+        if (A_ > 1 && mine > 1) fold(1, sr[1], up[1], rm[1]);
+        for (int n = 0; n < mine && ok; n += NS) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                if (n + i >= mine || !ok) break;
+                if (n + i + A_ < mine) fold(n + i + A_, sr[(i + A_) % NS], up[(i + A_) % NS], rm[(i + A_) % NS]);
+                if (ok) finish(n + i, sr[i], up[i], rm[i]);
+            }
         }
-        copy_empty(p.starts, p.T, p.n_seq, p.D, p.dh_last, p.dh0);
+        copy_empty<W>(p.starts, p.T, p.n_seq, p.D, p.dh_last, p.dh0);
     }
     if (!ok) let_copies_land();
     // this CTA's part of the rates' gradients, the warps in order
     __syncthreads();
-    if (w < kGWarps) sh.enter[0][w][lane] = ds;
+    if (w < W) sh.enter[0][w][lane] = neg(nds);
     __syncthreads();
     if (w == 0 && in) {
         float2 v = sh.enter[0][0][lane];
 #pragma unroll
-        for (int i = 1; i < kGWarps; ++i) v = __fadd2_rn(v, sh.enter[0][i][lane]);
+        for (int i = 1; i < W; ++i) v = __fadd2_rn(v, sh.enter[0][i][lane]);
         *reinterpret_cast<float2*>(p.part + (long long)turn * p.D + d) = v;
     }
 }
@@ -670,7 +737,7 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const UT* __restrict__ u,
     for (int j = 0; j < 4; j += 2) {
         float2 ka, kb;
         glr_row<false>(make_float2(r.v[j], r.v[j + 1]), make_float2(g.v[j], g.v[j + 1]), make_float2(x.v[j], x.v[j + 1]),
-                       make_float2(s.v[j], s.v[j + 1]), ka, kb);
+                       make_float2(-s.v[j], -s.v[j + 1]), ka, kb);
         y.v[j] = fmaf(ka.x, y.v[j], kb.x);
         y.v[j + 1] = fmaf(ka.y, y.v[j + 1], kb.y);
     }

@@ -83,8 +83,7 @@ pararnn_status check_starts(const void* starts)
 }
 
 // header | maps [tiles][S][32] (16 bytes each) | parts of the rates' gradients
-// [P][D].  Where CTAs share a slab the header is zeroed and the maps are set to
-// ones before each launch.
+// [P][D].  Where CTAs share a slab the maps are set to ones before each launch.
 struct GlrLayout {
     size_t maps, part, total;
     int S, tiles;
@@ -151,7 +150,6 @@ pararnn_status launch_glr(K kern, int threads, size_t smem, const GlrLayout& ly,
     p->wait_ns = kWaitLimitNs;
     const dim3 grid(unsigned(ly.S) * p->P);
     if (p->P > 1) {
-        CUDA_TRY(cudaMemsetAsync(ws, 0, ly.maps, st));
         CUDA_TRY(cudaMemsetAsync(base + ly.maps, 0xff, ly.part - ly.maps, st));
         CUDA_TRY(cudaLaunchCooperativeKernel(f, grid, dim3(threads), args, smem, st));
     } else {
@@ -168,7 +166,7 @@ pararnn_status launch_glr_scan(const UT* u, GlrParams p, long long D, void* ws, 
     CUtensorMap tu;
     TRY(map_glr(&tu, u, sizeof(UT) == 2 ? PARARNN_BF16 : PARARNN_F32, 3, p.T, D, LY::kTile));
     void* args[] = {(void*)&tu, (void*)&p};
-    return launch_glr(glr_scan_kernel<UT>, kGThreads, LY::smem_bytes, glr_layout(p.T, D, LY::kTile), &p, args, ws, st);
+    return launch_glr(glr_scan_kernel<UT>, LY::kThreads, LY::smem_bytes, glr_layout(p.T, D, LY::kTile), &p, args, ws, st);
 }
 
 template <class UT>
@@ -180,7 +178,7 @@ pararnn_status launch_glr_adjoint(const UT* u, GlrParams p, float* drate, long l
     TRY(map_glr(&th, p.states, PARARNN_F32, 1, p.T, D, LY::kTile));
     TRY(map_glr(&td, p.dh, PARARNN_F32, 1, p.T, D, LY::kTile));
     void* args[] = {(void*)&tu, (void*)&th, (void*)&td, (void*)&p};
-    TRY(launch_glr(glr_adjoint_kernel<UT>, kGThreads, LY::smem_bytes, glr_layout(p.T, D, LY::kTile), &p, args, ws, st));
+    TRY(launch_glr(glr_adjoint_kernel<UT>, LY::kThreads, LY::smem_bytes, glr_layout(p.T, D, LY::kTile), &p, args, ws, st));
     column_sum_kernel<<<unsigned((D + 31) / 32), 256, 0, st>>>(p.part, drate, p.P, D);
     return launched();
 }
