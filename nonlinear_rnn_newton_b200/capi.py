@@ -749,11 +749,12 @@ def _run(fn, dev, stream, *args):
         _check(st, allow=(OK,))
 
 
-def _space(nbytes, dev, workspace):
-    """(address, bytes) of the caller's workspace, or of a new one (kept by the
-    stream's order until the call's work is done); and the tensor."""
+def _space(nbytes, near, workspace):
+    """The caller's workspace or, on `near`'s device, a new one (freed in the
+    stream's order, so it lasts until the call's work is done), its address and
+    its bytes."""
     if workspace is None:
-        workspace = torch.empty(nbytes or 256, dtype=torch.uint8, device=dev)
+        workspace = near.new_empty(nbytes or 256, dtype=torch.uint8)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -799,14 +800,14 @@ def pararnn_glr_scan(u, rate, h0=None, seq_starts=None, h=None, h_last=None, wan
     shape, T, n_seq, D = _glr_args(u, rate, h0, seq_starts)
     dev = u.device
     if h is None:
-        h = torch.empty(shape, dtype=_f32, device=dev)
+        h = u.new_empty(shape, dtype=_f32)
     else:
         _fits(h, "h", shape, _f32, dev)
     if h_last is not None:
         _fits(h_last, "h_last", (n_seq, D), _f32, dev)
     elif want_last:
-        h_last = torch.empty((n_seq, D), dtype=_f32, device=dev)
-    ws, at, size = _space(lib.pararnn_glr_workspace_size(T, n_seq, D), dev, workspace)
+        h_last = u.new_empty((n_seq, D), dtype=_f32)
+    ws, at, size = _space(lib.pararnn_glr_workspace_size(T, n_seq, D), u, workspace)
     _run(lib.pararnn_glr_scan, dev, stream, u.data_ptr(), _CODES[u.dtype], rate.data_ptr(), _address(h0),
          _address(seq_starts), h.data_ptr(), _address(h_last), T, n_seq, D, at, size)
     return h, h_last
@@ -824,18 +825,18 @@ def pararnn_glr_adjoint(u, rate, h0, h, dh, dh_last=None, seq_starts=None, du=No
     if dh_last is not None:
         _fits(dh_last, "dh_last", (n_seq, D), _f32, dev)
     if du is None:
-        du = torch.empty(u.shape, dtype=_f32, device=dev)
+        du = u.new_empty(u.shape, dtype=_f32)
     else:
         _fits(du, "du", u.shape, _f32, dev)
     if drate is None:
-        drate = torch.empty((D,), dtype=_f32, device=dev)
+        drate = u.new_empty((D,), dtype=_f32)
     else:
         _fits(drate, "drate", (D,), _f32, dev)
     if dh0 is not None:
         _fits(dh0, "dh0", (n_seq, D), _f32, dev)
     elif want_dh0:
-        dh0 = torch.empty((n_seq, D), dtype=_f32, device=dev)
-    ws, at, size = _space(lib.pararnn_glr_adjoint_workspace_size(T, n_seq, D), dev, workspace)
+        dh0 = u.new_empty((n_seq, D), dtype=_f32)
+    ws, at, size = _space(lib.pararnn_glr_adjoint_workspace_size(T, n_seq, D), u, workspace)
     _run(lib.pararnn_glr_adjoint, dev, stream, u.data_ptr(), _CODES[u.dtype], rate.data_ptr(), _address(h0),
          _address(seq_starts), h.data_ptr(), dh.data_ptr(), _address(dh_last), du.data_ptr(), drate.data_ptr(),
          _address(dh0), T, n_seq, D, at, size)
@@ -856,7 +857,7 @@ def pararnn_glr_step(u, rate, h_prev=None, h_next=None, stream=None):
     if h_prev is not None:
         _fits(h_prev, "h_prev", (B, D), _f32, dev)
     if h_next is None:
-        h_next = torch.empty((B, D), dtype=_f32, device=dev)
+        h_next = u.new_empty((B, D), dtype=_f32) if h_prev is None else torch.empty_like(h_prev)
     else:
         _fits(h_next, "h_next", (B, D), _f32, dev)
     _run(lib.pararnn_glr_step, dev, stream, u.data_ptr(), code, rate.data_ptr(), _address(h_prev), h_next.data_ptr(), B,
@@ -890,25 +891,25 @@ def pararnn_rms_norm(x, w, residual=None, eps=1e-6, out_dtype=torch.bfloat16, su
         rc = _code(residual.dtype, "residual", _WIDE)
         _fits(residual, "residual", shape, residual.dtype, dev)
         if sum is None:
-            sum = torch.empty(shape, dtype=residual.dtype, device=dev)
+            sum = x.new_empty(shape, dtype=residual.dtype)
         else:
             _fits(sum, "sum", shape, residual.dtype, dev)
     elif sum is not None:
         raise ValueError("sum is an output of a call with a residual")
     if y is None:
-        y = torch.empty(shape, dtype=out_dtype, device=dev)
+        y = x.new_empty(shape, dtype=out_dtype)
     else:
         _fits(y, "y", shape, out_dtype, dev)
     if yc == E4M3:
         blocks = shape[:-1] + ((D + 127) // 128,)
         if y_scale is None:
-            y_scale = torch.empty(blocks, dtype=_f32, device=dev)
+            y_scale = x.new_empty(blocks, dtype=_f32)
         else:
             _fits(y_scale, "y_scale", blocks, _f32, dev)
     elif y_scale is not None:
         raise ValueError("y_scale is an output of an 8-bit call")
     if rstd is None:
-        rstd = torch.empty(shape[:-1], dtype=_f32, device=dev)
+        rstd = x.new_empty(shape[:-1], dtype=_f32)
     else:
         _fits(rstd, "rstd", shape[:-1], _f32, dev)
     _run(lib.pararnn_rms_norm, dev, stream, x.data_ptr(), xc, _address(residual), rc, w.data_ptr(), eps, _address(sum),
@@ -937,14 +938,14 @@ def pararnn_rms_norm_adjoint(dy, sum, w, rstd, dsum=None, dx=None, dw=None, work
     if dsum is not None:
         _fits(dsum, "dsum", shape, sum.dtype, dev)
     if dx is None:
-        dx = torch.empty(shape, dtype=sum.dtype, device=dev)
+        dx = sum.new_empty(shape, dtype=sum.dtype)
     else:
         _fits(dx, "dx", shape, sum.dtype, dev)
     if dw is None:
-        dw = torch.empty((D,), dtype=_f32, device=dev)
+        dw = sum.new_empty((D,), dtype=_f32)
     else:
         _fits(dw, "dw", (D,), _f32, dev)
-    ws, at, size = _space(lib.pararnn_rms_norm_adjoint_workspace_size(T, D), dev, workspace)
+    ws, at, size = _space(lib.pararnn_rms_norm_adjoint_workspace_size(T, D), sum, workspace)
     _run(lib.pararnn_rms_norm_adjoint, dev, stream, dy.data_ptr(), yc, sum.data_ptr(), sc, w.data_ptr(),
          rstd.data_ptr(), _address(dsum), dx.data_ptr(), dw.data_ptr(), T, D, at, size)
     return dx, dw
@@ -968,11 +969,11 @@ def pararnn_fp8_quantize(x, block_rows=1, q=None, scale=None, stream=None):
     else:
         raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
     if q is None:
-        q = torch.empty(shape, dtype=_e4m3, device=dev)
+        q = x.new_empty(shape, dtype=_e4m3)
     else:
         _fits(q, "q", shape, _e4m3, dev)
     if scale is None:
-        scale = torch.empty(blocks, dtype=_f32, device=dev)
+        scale = x.new_empty(blocks, dtype=_f32)
     else:
         _fits(scale, "scale", blocks, _f32, dev)
     _run(lib.pararnn_fp8_quantize, dev, stream, x.data_ptr(), xc, block_rows, q.data_ptr(), scale.data_ptr(), M, K)
@@ -1001,10 +1002,10 @@ def pararnn_fp8_project(x, x_scale, w, w_scale, bias=None, out_dtype=torch.bfloa
     if bias is not None:
         _fits(bias, "bias", (N,), _f32, dev)
     if u is None:
-        u = torch.empty(shape[:-1] + (N,), dtype=out_dtype, device=dev)
+        u = x.new_empty(shape[:-1] + (N,), dtype=out_dtype)
     else:
         _fits(u, "u", shape[:-1] + (N,), out_dtype, dev)
-    ws, at, size = _space(lib.pararnn_fp8_project_workspace_size(M, N, K), dev, workspace)
+    ws, at, size = _space(lib.pararnn_fp8_project_workspace_size(M, N, K), x, workspace)
     _run(lib.pararnn_fp8_project, dev, stream, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
          _address(bias), u.data_ptr(), uc, M, N, K, at, size)
     return u

@@ -11,10 +11,14 @@
 // Both are bound by HBM: a row is read once into registers (8 columns a
 // vector, NV vectors a thread) and everything else happens there.  A row
 // belongs to `tpr` threads (a multiple of 32); 16 neighbouring lanes hold one
-// block of 128 columns, so its scale needs four shuffles.
+// block of 128 columns, so its scale needs four shuffles.  The norm of T 32768
+// D 2048 (fp32 in, bf16 residual, e4m3 out) takes 92 us, 6.5 TB/s, as much as a
+// copy.
 #pragma once
 
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "device_common.cuh"
 
@@ -71,6 +75,24 @@ struct Raw8<void> {  // absent: zeros
     }
 };
 
+// Arithmetic on pairs of neighbouring columns, in the packed fp32 instructions.
+struct P8 {
+    float2 v[4];
+};
+
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+
+template <class R>
+__device__ __forceinline__ P8 pairs(const R& raw)
+{
+    float x[8];
+    raw.get(x);
+    P8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = make_float2(x[2 * i], x[2 * i + 1]);
+    return r;
+}
+
 // two bf16, rounded to nearest even, the first in the low half
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
 {
@@ -79,33 +101,33 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return r;
 }
 
-__device__ __forceinline__ void store8(void* p, long long i, bool bf16, const float (&v)[8])
+__device__ __forceinline__ void store8(void* p, long long i, bool bf16, const P8& x)
 {
     if (bf16) {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
-            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+            make_uint4(pack_bf16x2(x.v[0].x, x.v[0].y), pack_bf16x2(x.v[1].x, x.v[1].y), pack_bf16x2(x.v[2].x, x.v[2].y),
+                       pack_bf16x2(x.v[3].x, x.v[3].y));
     } else {
         float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-        q[0] = make_float4(v[0], v[1], v[2], v[3]);
-        q[1] = make_float4(v[4], v[5], v[6], v[7]);
+        q[0] = make_float4(x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y);
+        q[1] = make_float4(x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y);
     }
 }
 
 // eight e4m3, rounded to nearest even, NaN kept
-__device__ __forceinline__ uint2 pack_e4m3x8(const float (&v)[8])
+__device__ __forceinline__ uint2 pack_e4m3x8(const P8& x)
 {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 4; ++i) w[i] = __nv_cvt_float2_to_fp8x2(x.v[i], __NV_SATFINITE, __NV_E4M3);
     return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-__device__ __forceinline__ float amax8(const float (&v)[8])
+__device__ __forceinline__ float amax8(const P8& x)
 {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max_keep_nan(m, fabsf(v[i]));
+    for (int i = 0; i < 4; ++i) m = max_keep_nan(max_keep_nan(m, fabsf(x.v[i].x)), fabsf(x.v[i].y));
     return m;
 }
 
@@ -157,52 +179,56 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormParams
     const int tpr = p.tpr, rows = blockDim.x / tpr;
     const int lane = threadIdx.x % tpr;
     const long long t = (long long)blockIdx.x * rows + threadIdx.x / tpr;
-    const bool live = t < p.T;
     const long long D = p.D, base = t * D;
+    const int left = t < p.T ? int(D) - 8 * lane : 0;  // vector k is in the row where 8 k tpr < left
     Raw8<XT> rx[NV];
     Raw8<RT> rr[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const long long c = 8ll * (lane + k * tpr);
-        if (live && c < D) {
-            rx[k].load(p.x, base + c);
-            rr[k].load(p.res, base + c);
+        if (8 * k * tpr < left) {
+            rx[k].load(p.x, base + 8 * (lane + k * tpr));
+            rr[k].load(p.res, base + 8 * (lane + k * tpr));
         }
     }
-    float v[NV][8], ss = 0.f;
+    P8 v[NV];
+    float2 ss = twice(0.f);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const long long c = 8ll * (lane + k * tpr);
-        const bool in = live && c < D;
-        float r[8];
-        rx[k].get(v[k]);
-        rr[k].get(r);
+        const bool in = 8 * k * tpr < left;
+        v[k] = pairs(rx[k]);
+        if constexpr (!std::is_void<RT>::value) {
+            const P8 r = pairs(rr[k]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[k][j] = in ? v[k][j] + r[j] : 0.f;
-            ss = fmaf(v[k][j], v[k][j], ss);
+            for (int j = 0; j < 4; ++j) v[k].v[j] = __fadd2_rn(v[k].v[j], r.v[j]);
         }
-        if (in && p.sum) store8(p.sum, base + c, p.sum_bf16, v[k]);
+        if (in) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ss = __ffma2_rn(v[k].v[j], v[k].v[j], ss);
+            if (p.sum) store8(p.sum, base + 8 * (lane + k * tpr), p.sum_bf16, v[k]);
+        }
     }
-    ss = row_sum(ss, tpr, s_red);
-    const float rstd = 1.0f / sqrtf(ss / float(D) + p.eps);
-    if (live && lane == 0 && p.rstd) p.rstd[t] = rstd;
+    const float all = row_sum(ss.x + ss.y, tpr, s_red);
+    const float rstd = 1.0f / sqrtf(all / float(D) + p.eps);
+    if (left > 0 && lane == 0 && p.rstd) p.rstd[t] = rstd;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const long long c = 8ll * (lane + k * tpr);
-        const bool in = live && c < D;
-        float y[8];
+        const int c = 8 * (lane + k * tpr);
+        const bool in = 8 * k * tpr < left;
+        P8 y;
         if (in) {
             Raw8<float> rw;
             rw.load(p.w, c);
-            rw.get(y);
+            y = pairs(rw);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = in ? v[k][j] * rstd * y[j] : 0.f;
+        for (int j = 0; j < 4; ++j) y.v[j] = in ? __fmul2_rn(__fmul2_rn(v[k].v[j], twice(rstd)), y.v[j]) : twice(0.f);
         if (p.y_dtype == PARARNN_E4M3) {
             const float sc = scale_of(max16(amax8(y)));
+            // one reciprocal a block: a division for each value took as long
+            // as the memory (T 32768 D 2048: 122 us)
+            const float2 inv = twice(1.0f / sc);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = y[j] / sc;
+            for (int j = 0; j < 4; ++j) y.v[j] = __fmul2_rn(y.v[j], inv);
             if (in) {
                 *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + base + c) = pack_e4m3x8(y);
                 if ((lane & 15) == 0) p.scale[t * ((D + 127) / 128) + c / 128] = sc;
@@ -223,8 +249,11 @@ struct NormAdjParams {
     int tpr;
 };
 
-// A CTA takes rows blockIdx.x * rows + k * gridDim.x * rows; dw of its rows
-// stays in registers and leaves once, one row of `part` a CTA.
+// A CTA takes rows blockIdx.x * rows + k * gridDim.x * rows, and asks for its
+// next row before it works on this one; dw of its rows stays in registers and
+// leaves once, one row of `part` a CTA.  T 32768 D 2048, bf16: 98 us, 5.5 TB/s
+// (without the loads ahead 120 us); a row's two loads of three arrays by 128
+// threads, five CTAs an SM, are about 60 KB in flight on an SM.
 template <class YT, class VT, int NV>
 __global__ void __launch_bounds__(kNormThreads) rms_norm_adjoint_kernel(const NormAdjParams p)
 {
@@ -232,71 +261,82 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_adjoint_kernel(const No
     extern __shared__ float s_dw[];  // [rows][D] where a CTA has several rows
     const int tpr = p.tpr, rows = blockDim.x / tpr, row = threadIdx.x / tpr;
     const int lane = threadIdx.x % tpr;
-    const long long D = p.D;
-    float dw[NV][8];
+    const long long D = p.D, step = (long long)gridDim.x * rows;
+    const int left = int(D) - 8 * lane;
+    P8 dw[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) dw[k][j] = 0.f;
-    int turn = 0;
-    for (long long t0 = (long long)blockIdx.x * rows; t0 < p.T; t0 += (long long)gridDim.x * rows, turn ^= 1) {
-        const long long t = t0 + row, base = t * D;
-        const bool live = t < p.T;
-        Raw8<YT> ry[NV];
-        Raw8<VT> rv[NV], rd[NV];
+        for (int j = 0; j < 4; ++j) dw[k].v[j] = twice(0.f);
+    Raw8<YT> ry[NV];
+    Raw8<VT> rv[NV], rd[NV];
+    float rstd = 0.f;
+    auto load = [&](long long t) {
+        if (t >= p.T) return;
+        rstd = __ldg(p.rstd + t);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const long long c = 8ll * (lane + k * tpr);
-            if (live && c < D) {
-                ry[k].load(p.dy, base + c);
-                rv[k].load(p.v, base + c);
-                if (p.dv) rd[k].load(p.dv, base + c);
+            const long long c = t * D + 8 * (lane + k * tpr);
+            if (8 * k * tpr < left) {
+                ry[k].load(p.dy, c);
+                rv[k].load(p.v, c);
+                if (p.dv) rd[k].load(p.dv, c);
             }
         }
-        const float rstd = live ? p.rstd[t] : 0.f;
-        float g[NV][8], n[NV][8], gn = 0.f;
+    };
+    // four vectors a thread leave no registers for a second row's loads
+    constexpr bool kAhead = NV <= 2;
+    int turn = 0;
+    long long t0 = (long long)blockIdx.x * rows;
+    if (kAhead) load(t0 + row);
+    for (; t0 < p.T; t0 += step, turn ^= 1) {
+        const long long t = t0 + row, base = t * D;
+        const bool live = t < p.T;
+        if (!kAhead) load(t);
+        const float rs = live ? rstd : 0.f;
+        P8 g[NV], n[NV], d[NV];
+        float2 gn2 = twice(0.f);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const long long c = 8ll * (lane + k * tpr);
-            const bool in = live && c < D;
-            ry[k].get(g[k]);
-            rv[k].get(n[k]);
-            float w[8];
-            if (in) {
-                Raw8<float> rw;
-                rw.load(p.w, c);
-                rw.get(w);
-            }
+            g[k] = pairs(ry[k]);
+            n[k] = pairs(rv[k]);
+            if (p.dv) d[k] = pairs(rd[k]);
+        }
+        if (kAhead) load(t + step);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                n[k][j] = in ? n[k][j] * rstd : 0.f;
-                const float dy = in ? g[k][j] : 0.f;
-                dw[k][j] = fmaf(dy, n[k][j], dw[k][j]);
-                g[k][j] = in ? dy * w[j] : 0.f;
-                gn = fmaf(g[k][j], n[k][j], gn);
+        for (int k = 0; k < NV; ++k) {
+            if (live && 8 * k * tpr < left) {
+                Raw8<float> rw;
+                rw.load(p.w, 8 * (lane + k * tpr));
+                const P8 w = pairs(rw);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    n[k].v[j] = __fmul2_rn(n[k].v[j], twice(rs));
+                    dw[k].v[j] = __ffma2_rn(g[k].v[j], n[k].v[j], dw[k].v[j]);
+                    g[k].v[j] = __fmul2_rn(g[k].v[j], w.v[j]);
+                    gn2 = __ffma2_rn(g[k].v[j], n[k].v[j], gn2);
+                }
             }
         }
         // two buffers in turn: a warp may be a row ahead of one still summing
-        gn = row_sum(gn, tpr, s_red[turn]) / float(D);
+        const float mean = row_sum(gn2.x + gn2.y, tpr, s_red[turn]) / float(D);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const long long c = 8ll * (lane + k * tpr);
-            if (live && c < D) {
-                float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (p.dv) rd[k].get(o);
+            if (live && 8 * k * tpr < left) {
+                P8 o;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = fmaf(rstd, fmaf(-n[k][j], gn, g[k][j]), o[j]);
-                store8(p.dx, base + c, sizeof(VT) == 2, o);
+                for (int j = 0; j < 4; ++j) {
+                    o.v[j] = __ffma2_rn(n[k].v[j], twice(-mean), g[k].v[j]);
+                    o.v[j] = p.dv ? __ffma2_rn(twice(rs), o.v[j], d[k].v[j]) : __fmul2_rn(twice(rs), o.v[j]);
+                }
+                store8(p.dx, base + 8 * (lane + k * tpr), sizeof(VT) == 2, o);
             }
         }
     }
     if (rows > 1) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const long long c = 8ll * (lane + k * tpr);
-            if (c < D)
-                for (int j = 0; j < 8; ++j) s_dw[row * D + c + j] = dw[k][j];
-        }
+        for (int k = 0; k < NV; ++k)
+            if (8 * k * tpr < left) store8(s_dw, row * D + 8 * (lane + k * tpr), false, dw[k]);
         __syncthreads();
         for (long long c = threadIdx.x; c < D; c += blockDim.x) {
             float a = 0.f;
@@ -305,10 +345,8 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_adjoint_kernel(const No
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const long long c = 8ll * (lane + k * tpr);
-            if (c < D) store8(p.part, (long long)blockIdx.x * D + c, false, dw[k]);
-        }
+        for (int k = 0; k < NV; ++k)
+            if (8 * k * tpr < left) store8(p.part, (long long)blockIdx.x * D + 8 * (lane + k * tpr), false, dw[k]);
     }
 }
 
@@ -322,15 +360,17 @@ __global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const void* x, u
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;  // 8 columns of a row filled up to whole blocks
     const long long m = i / (KB * 16), c = 8 * (i - m * KB * 16);
     const bool in = m < M && c < K;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    P8 v = {{twice(0.f), twice(0.f), twice(0.f), twice(0.f)}};
     if (in) {
         Raw8<XT> r;
         r.load(x, m * K + c);
-        r.get(v);
+        v = pairs(r);
     }
     const float sc = scale_of(max16(amax8(v)));
+    // divided, not multiplied by a reciprocal: bf16 values often lie halfway
+    // between two e4m3 ones, and the rounded quotient then decides
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = v[j] / sc;
+    for (int j = 0; j < 4; ++j) v.v[j] = make_float2(v.v[j].x / sc, v.v[j].y / sc);
     if (in) {
         *reinterpret_cast<uint2*>(q + m * K + c) = pack_e4m3x8(v);
         if ((threadIdx.x & 15) == 0) scale[m * KB + c / 128] = sc;
@@ -349,11 +389,12 @@ __global__ void __launch_bounds__(256) fp8_quantize_blocks_kernel(const void* x,
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (m0 + 16 * i < M && c < K) r[i].load(x, (m0 + 16 * i) * K + c);
-    float v[8][8], most = 0.f;
+    P8 v[8];
+    float most = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (m0 + 16 * i < M && c < K) {
-            r[i].get(v[i]);
+            v[i] = pairs(r[i]);
             most = max_keep_nan(most, amax8(v[i]));
         }
     most = max16(most);
@@ -367,7 +408,7 @@ __global__ void __launch_bounds__(256) fp8_quantize_blocks_kernel(const void* x,
     for (int i = 0; i < 8; ++i)
         if (m0 + 16 * i < M && c < K) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] / sc;
+            for (int j = 0; j < 4; ++j) v[i].v[j] = make_float2(v[i].v[j].x / sc, v[i].v[j].y / sc);
             *reinterpret_cast<uint2*>(q + (m0 + 16 * i) * K + c) = pack_e4m3x8(v[i]);
         }
     if (threadIdx.x == 0) scale[blockIdx.x] = sc;
