@@ -156,24 +156,7 @@ __device__ __forceinline__ void let_copies_land()
     while (global_timer_ns() - t0 < 2000000ull) __nanosleep(1000);
 }
 
-// 32 consecutive fp32 columns of this warp's 32 TMEM lanes (one per thread)
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32])
-{
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// 16 of them
+// 16 consecutive fp32 columns of this warp's 32 TMEM lanes (one per thread)
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[16])
 {
     uint32_t r[16];
@@ -186,19 +169,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[16])
         : "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// (a0, a1) + s (t0, t1) in one packed instruction
-__device__ __forceinline__ void fma2(float& a0, float& a1, float t0, float t1, float s0, float s1)
-{
-    asm("{\n\t.reg .b64 a, t, s;\n\t"
-        "mov.b64 a, {%0, %1};\n\t"
-        "mov.b64 t, {%2, %3};\n\t"
-        "mov.b64 s, {%4, %5};\n\t"
-        "fma.rn.f32x2 a, t, s, a;\n\t"
-        "mov.b64 {%0, %1}, a;\n\t}"
-        : "+f"(a0), "+f"(a1)
-        : "f"(t0), "f"(t1), "f"(s0), "f"(s1));
 }
 
 struct Fp8Params {
@@ -228,18 +198,28 @@ __device__ __forceinline__ void clear_outcome(WsHeader* hdr)
 // Many rows: a pair of CTAs (cta_group::2, M = 256, N = 256) owns a tile of 256
 // rows x 256 columns; each CTA loads its 128 rows of x and 128 of the 256 rows
 // of w and ends up with its own rows' sums.  Warps: 0 loads, 1 issues the
-// products (in the leading CTA), 4..11 read the accumulators, a row a thread
-// and 128 columns a warp: 128 running sums and two loads of 32 columns in
-// registers, for which the other warps hand theirs over (setmaxnreg: 128 x 40
-// + 256 x 232 = 384 x 168, what the kernel is launched with).
+// products (in the leading CTA), 4..19 read the accumulators, a row a thread
+// and 64 columns a warp: 64 running sums and two loads of 16 columns in
+// registers, for which the other warps hand theirs over (setmaxnreg: 128 x 32
+// + 512 x 112 = 640 x 96, what the kernel is launched with).
+//
+// What bounds it: reading and scaling the accumulators.  M 32768 N 6144 K 2048
+// takes 448 us (1.84 PFLOP/s, 1.1 of a bf16 product's measured peak); the same
+// kernel that only multiplies, without waiting for its accumulators to be read,
+// takes 333.  Eight reading warps of 128 columns: 474 us; products of 128
+// columns with four accumulators: 500; one CTA with 128 x 256 tiles: 472.
 constexpr int kQM = 128;       // rows of x a CTA (256 a pair)
 constexpr int kQN = 256;       // columns of a pair's tile
-constexpr int kQThreads = 384;
+constexpr int kQEpi = 16;                // warps that read accumulators
+constexpr int kQCols = kQN * 4 / kQEpi;  // columns a warp
+constexpr int kQChunk = 16;              // of which a load brings this many
+constexpr int kQThreads = 32 * (4 + kQEpi);
 constexpr int kQAhead = 4;     // blocks that a thread fetches its scales ahead
 constexpr int kQStages = 5;
 constexpr size_t kQStageBytes = size_t(kQM + kQN / 2) * kQK;
 constexpr size_t kQOut = kQStages * kQStageBytes;  // 2 x 4 KB a reading warp
-constexpr size_t kQBar = kQOut + 8 * 8192;
+constexpr int kQOutBufs = 16 / kQEpi;
+constexpr size_t kQBar = kQOut + 16 * 4096;
 constexpr size_t kQSmem = kQBar + (2 * kQStages + 4) * 8 + 16 + 1024;
 static_assert(kQSmem <= 232448, "shared memory");
 
@@ -265,38 +245,29 @@ __device__ __forceinline__ void tma_store_wait_read()
 // (two in turn) in the 128-byte swizzle (16-byte piece i of row r at i ^ (r %
 // 8): eight rows' writes fall in distinct banks) and a bulk store of the
 // piece.  Writing the rows from registers, 16 bytes a row and instruction,
-// took 250 of 650 us at M 32768, N 6144, K 2048.  Lane l holds the bias of
-// columns 4 l .. 4 l + 3.
+// took 250 of 650 us at M 32768, N 6144, K 2048.
 template <bool Bf16>
 __device__ __forceinline__ void store_sums(const Fp8Params& p, const CUtensorMap* tm_u, unsigned char* stage, int m0,
-                                           int n0, int lane, float4 bias, float (&acc)[128])
+                                           int n0, int lane, const float2 (&acc)[kQCols / 2])
 {
     constexpr int kCols = Bf16 ? 64 : 32;  // columns of a piece
     constexpr int kPer = kCols / 8;        // columns of 16 bytes
-    if (p.bias) {
 #pragma unroll
-        for (int j = 0; j < 128; j += 4) {
-            acc[j] += __shfl_sync(0xffffffffu, bias.x, j / 4);
-            acc[j + 1] += __shfl_sync(0xffffffffu, bias.y, j / 4);
-            acc[j + 2] += __shfl_sync(0xffffffffu, bias.z, j / 4);
-            acc[j + 3] += __shfl_sync(0xffffffffu, bias.w, j / 4);
-        }
-    }
-#pragma unroll
-    for (int c = 0; c < 128; c += kCols) {
+    for (int c = 0; c < kQCols; c += kCols) {
         if (n0 + c >= p.N) break;
-        unsigned char* buf = stage + (c / kCols & 1) * 4096;
-        if (lane == 0) tma_store_wait_read<1>();  // the piece before the last has left
+        unsigned char* buf = stage + (kQOutBufs > 1 ? (c / kCols & 1) * 4096 : 0);
+        if (lane == 0) tma_store_wait_read<kQOutBufs - 1>();  // the piece that was there has left
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float* v = acc + c + i * kPer;
+            const float2* v = acc + (c + i * kPer) / 2;
             uint4 o;
             if constexpr (Bf16)
-                o = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                               pack_bf16x2(v[6], v[7]));
+                o = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                               pack_bf16x2(v[3].x, v[3].y));
             else
-                o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+                o = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
+                               __float_as_uint(v[1].y));
             *reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) = o;
         }
         fence_proxy_async_shared();
@@ -331,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], 2 * 8);
+            mbar_init(&tempty[i], 2 * kQEpi);
         }
         fence_mbar_init();
         prefetch_tensormap(&tm_x);
@@ -345,7 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
     const uint32_t tmem = *s_tmem;
 
     if (w < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(32));
         if (w == 0 && lane == 0) {
             int q = 0;
             for (int t = pair; t < p.n_tiles && ok; t += pairs) {
@@ -388,23 +359,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-        const int lq = w & 3, half = (w >> 2) - 1;
-        const uint32_t ta = tmem + (uint32_t(32 * lq) << 16) + uint32_t(half) * 128;
-        unsigned char* out = smem + kQOut + (w - 4) * 8192;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(112));
+        const int lq = w & 3, part = (w >> 2) - 1;
+        const uint32_t ta = tmem + (uint32_t(32 * lq) << 16) + uint32_t(part) * kQCols;
+        unsigned char* out = smem + kQOut + (w - 4) * 4096 * kQOutBufs;
         int q = 0;
         for (int t = pair; t < p.n_tiles && ok; t += pairs) {
             const int tm = t / p.tiles_n, tn = t - tm * p.tiles_n;
             const long long m = (long long)tm * 2 * kQM + rank * kQM + 32 * lq + lane;
-            const long long n = (long long)tn * kQN + half * 128;
+            const long long n = (long long)tn * kQN + part * kQCols;
             const bool in = m < p.M && n < p.N;
             const float* xs = p.xs + m * p.KB;
             const float* ws = p.ws + n / 128 * p.KB;
-            float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (p.bias && n + 4 * lane < p.N) bias = __ldg(reinterpret_cast<const float4*>(p.bias + n) + lane);
-            float acc[128];
+            float2 acc[kQCols / 2];  // from the bias on
 #pragma unroll
-            for (int j = 0; j < 128; ++j) acc[j] = 0.f;
+            for (int j = 0; j < kQCols; j += 4) {
+                float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (p.bias && n + j < p.N) bias = __ldg(reinterpret_cast<const float4*>(p.bias + n + j));
+                acc[j / 2] = make_float2(bias.x, bias.y);
+                acc[j / 2 + 1] = make_float2(bias.z, bias.w);
+            }
             float sx[kQAhead], sw[kQAhead];  // scales of the blocks from kb on
 #pragma unroll
             for (int i = 0; i < kQAhead; ++i) {
@@ -425,29 +399,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
                 ok = __all_sync(0xffffffffu, mbar_wait_clocked(&tfull[b], uint32_t(q / 2) & 1u, err, p.wait_ns));
                 if (!ok) break;
                 tc_fence_after();
-                float v[2][32];
-                const uint32_t tb = ta + uint32_t(q & 1) * 256;
+                float v[2][kQChunk];
+                const uint32_t tb = ta + uint32_t(q & 1) * kQN;
+                constexpr int kChunks = kQCols / kQChunk;
                 tmem_ld(tb, v[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < kChunks; ++c) {
                     tmem_wait_ld();
-                    if (c < 3) {
-                        tmem_ld(tb + 32 * (c + 1), v[(c + 1) & 1]);
-                    } else {
+                    if (c + 1 < kChunks) tmem_ld(tb + kQChunk * (c + 1), v[(c + 1) & 1]);
+                    if (c + 1 == kChunks) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(mapa(&tempty[b], 0));
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2)
-                        { acc[32*c+j]=fmaf(v[c&1][j],sc,acc[32*c+j]); acc[32*c+j+1]=fmaf(v[c&1][j+1],sc,acc[32*c+j+1]); }
+                    for (int j = 0; j < kQChunk; j += 2) {
+                        float2& s = acc[(kQChunk * c + j) / 2];
+                        s = __ffma2_rn(make_float2(v[c & 1][j], v[c & 1][j + 1]), make_float2(sc, sc), s);
+                    }
                 }
             }
             if (ok) {
                 const int m0 = tm * 2 * kQM + int(rank) * kQM + 32 * lq;
                 if (m0 < p.M && n < p.N) {
-                    if (p.u_bf16) store_sums<true>(p, &tm_u, out, m0, int(n), lane, bias, acc);
-                    else store_sums<false>(p, &tm_u, out, m0, int(n), lane, bias, acc);
+                    if (p.u_bf16) store_sums<true>(p, &tm_u, out, m0, int(n), lane, acc);
+                    else store_sums<false>(p, &tm_u, out, m0, int(n), lane, acc);
                 }
             }
         }
@@ -468,13 +444,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
 // loads in flight.  Their sums meet in shared memory (each CTA adds a slice of
 // the tile over the cluster's CTAs in rank order, so the order is fixed).
 // Warps: 0 loads, 1 issues the products, 2..5 read the accumulators.
+// M 16 N 6144 K 2048 takes 6.6 us of which its 12.6 MB need 1.9; N 2048 K 8192
+// 8.2 us (16.8 MB, 2.6 us): the launch, the first loads' way and the cluster's
+// two meetings are about 5 us.
 constexpr int kNThreads = 32 * 6;
 constexpr int kNScaleBlocks = 16;  // blocks whose scales are in shared memory at a time
 
 template <int NT>
 struct NarrowLayout {
     static constexpr size_t stage_bytes = size_t(128 + NT) * kQK;
-    static constexpr int kStages = NT >= 128 ? 6 : NT >= 64 ? 4 : 5;
+    static constexpr int kStages = NT >= 64 ? 4 : 5;  // two CTAs fit on an SM
     static constexpr size_t off_scale = kStages * stage_bytes;  // [kNScaleBlocks][NT] xs ws
     static constexpr size_t off_bar = off_scale + size_t(kNScaleBlocks) * NT * 4;
     static constexpr size_t smem_bytes = off_bar + (2 * kStages + 4) * 8 + 16 + 1024;
@@ -527,9 +506,9 @@ __global__ void __launch_bounds__(kNThreads)
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
 
-    float acc[NT];
+    float2 acc[NT / 2];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) acc[j] = 0.f;
+    for (int j = 0; j < NT / 2; ++j) acc[j] = make_float2(0.f, 0.f);
 
     if (w == 0) {
         if (lane == 0) {
@@ -595,8 +574,9 @@ __global__ void __launch_bounds__(kNThreads)
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
                     const float4 s4 = *reinterpret_cast<const float4*>(sc + 16 * c + j);
-                    fma2(acc[16 * c + j], acc[16 * c + j + 1], v[j], v[j + 1], s4.x, s4.y);
-                    fma2(acc[16 * c + j + 2], acc[16 * c + j + 3], v[j + 2], v[j + 3], s4.z, s4.w);
+                    float2* s = acc + (16 * c + j) / 2;
+                    s[0] = __ffma2_rn(make_float2(v[j], v[j + 1]), make_float2(s4.x, s4.y), s[0]);
+                    s[1] = __ffma2_rn(make_float2(v[j + 2], v[j + 3]), make_float2(s4.z, s4.w), s[1]);
                 }
             }
             tc_fence_before();
@@ -607,7 +587,7 @@ __global__ void __launch_bounds__(kNThreads)
         float* red = reinterpret_cast<float*>(smem);
         if (ok) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) red[j * 128 + 32 * lq + lane] = acc[j];
+            for (int j = 0; j < NT; ++j) red[j * 128 + 32 * lq + lane] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
         }
     }
     if (!ok) let_copies_land();

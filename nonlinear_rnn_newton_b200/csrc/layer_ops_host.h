@@ -325,8 +325,20 @@ pararnn_status launch_clusters(K kern, int grid, int threads, int cluster, size_
     return PARARNN_OK;
 }
 
+// How many CTAs of the narrow form share a tile's blocks of K: as long as all
+// of them run at once (two an SM, less what clusters of up to eight leave over:
+// 288 in clusters of four took two rounds, 256 one).
+constexpr long long kNarrowRoom = 256;
+
+int narrow_splits(long long tiles, long long KB)
+{
+    int splits = 1;
+    while (splits < 8 && splits * 2 <= KB && tiles * splits * 2 <= kNarrowRoom) splits *= 2;
+    return splits;
+}
+
 template <int NT>
-pararnn_status launch_narrow(const uint8_t* x, const uint8_t* w, Fp8Params p, int sms, cudaStream_t st)
+pararnn_status launch_narrow(const uint8_t* x, const uint8_t* w, Fp8Params p, cudaStream_t st)
 {
     using LY = NarrowLayout<NT>;
     CUtensorMap tx, tw;
@@ -336,10 +348,7 @@ pararnn_status launch_narrow(const uint8_t* x, const uint8_t* w, Fp8Params p, in
     const long long tiles = (p.M + NT - 1) / NT * p.tiles_n;
     if (tiles > INT_MAX / 8) return fail(PARARNN_ERR_INVALID_ARG, "too many tiles");
     p.n_tiles = int(tiles);
-    // as many CTAs as there are SMs, twice over where two fit
-    const int room = sms * (LY::smem_bytes * 2 <= 227 * 1024 ? 2 : 1);
-    p.splits = 1;
-    while (p.splits < 8 && p.splits * 2 <= p.KB && tiles * p.splits * 2 <= room) p.splits *= 2;
+    p.splits = narrow_splits(tiles, p.KB);
     void* args[] = {(void*)&tx, (void*)&tw, (void*)&p};
     return launch_clusters(fp8_project_narrow_kernel<NT>, p.n_tiles * p.splits, kNThreads, p.splits, LY::smem_bytes, st, args);
 }
@@ -634,11 +643,22 @@ pararnn_status pararnn_fp8_project(const void* x, const float* x_scale, const vo
     p.wait_ns = kWaitLimitNs;
     const uint8_t *xb = static_cast<const uint8_t*>(x), *wb = static_cast<const uint8_t*>(w);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-        if (M >= 256) return launch_wide(xb, wb, p, sms, st);
-    if (M > 64) return launch_narrow<128>(xb, wb, p, sms, st);
-    if (M > 32) return launch_narrow<64>(xb, wb, p, sms, st);
-    if (M > 16) return launch_narrow<32>(xb, wb, p, sms, st);
-    return launch_narrow<16>(xb, wb, p, sms, st);
+        // Blocks of K one after another in the fullest CTA, and what one costs: a
+    // pair's 0.53 us each and 5.5 us before and after, the narrow form's (64
+    // rows) 0.65 and 6.  N 6144 K 2048: 12.6 (narrow) against 14.2 us at M 128,
+    // 15.8 against 14.4 at M 200; N 2048 K 8192: 25.9 against 39.7 at M 512,
+    // 43.0 against 40.0 at M 768.
+    const long long pairs = std::max(1, sms / 2);
+    const long long wide_tiles = (M + 2 * kQM - 1) / (2 * kQM) * ((N + kQN - 1) / kQN);
+    const long long tiles = (M + 63) / 64 * blocks128(N);
+    const int splits = narrow_splits(tiles, KB);
+    const double wide_us = 5.5 + 0.53 * double((wide_tiles + pairs - 1) / pairs * KB);
+    const double narrow_us = 6.0 + 0.65 * double((tiles * splits + kNarrowRoom - 1) / kNarrowRoom * ((KB + splits - 1) / splits));
+    if (M > 64 && wide_us < narrow_us) return launch_wide(xb, wb, p, sms, st);
+    if (M > 64) return launch_narrow<64>(xb, wb, p, st);
+    // up to 64 rows: 32 a CTA also for 33 to 64 (N 2048 K 8192, M 64: 10.7 against 12.0 us)
+    if (M > 16) return launch_narrow<32>(xb, wb, p, st);
+    return launch_narrow<16>(xb, wb, p, st);
 }
 
 }  // extern "C"

@@ -356,7 +356,7 @@ def test_quantize_bad_values_stay_in_their_block(cuda, rows, bad):
 
 SIZES = [(1, 8, 16), (1, 200, 128), (3, 136, 144), (16, 256, 512), (17, 264, 1040), (64, 1304, 272), (65, 128, 128),
          (100, 392, 2048), (127, 256, 640), (128, 128, 384), (129, 264, 400), (200, 1000, 1104), (300, 520, 4096),
-         (513, 2056, 656), (1000, 768, 256)]
+         (513, 2056, 656), (1000, 768, 256), (300, 8200, 1040), (2570, 2056, 400)]
 
 
 @pytest.mark.parametrize("u", [BF16, F32], ids=["bf16", "f32"])
