@@ -123,13 +123,13 @@ __device__ __forceinline__ RowSeq row_seq(const int* starts, int T, int n_seq, i
     int lo = -1, hi = n_seq + 1;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(starts + mid) <= t) lo = mid;
+        if (starts[mid] <= t) lo = mid;
         else hi = mid;
     }
     if (lo < 0 || lo >= n_seq) return r;
     r.owner = lo;
-    r.first = max(__ldg(starts + lo), 0) == t;
-    r.last = min(__ldg(starts + lo + 1), T) == t + 1;
+    r.first = max(starts[lo], 0) == t;
+    r.last = min(starts[lo + 1], T) == t + 1;
     return r;
 }
 
@@ -210,6 +210,8 @@ __device__ __forceinline__ float2 apply(const Map2& m, float2 y)
     return m.cut ? m.b : __ffma2_rn(m.a, y, m.b);
 }
 
+constexpr int kGStarts = 1025;  // offsets kept in shared memory
+
 // The shared parts of both scans' shared memory behind the stages.
 constexpr int kGMaxStages = 5;
 template <int W, int NS>  // computing warps, folded tiles at a time
@@ -221,7 +223,20 @@ struct GlrShared {
     uint64_t full[kGMaxStages], empty[kGMaxStages];
     float2 own[2][32];            // the state that tile n ended with, at n % 2
     uint64_t agg_full[NS], entered[2], passed[2];
+    int starts[kGStarts];         // the sequences' offsets, where they fit
 };
+
+// The sequences' offsets in shared memory if there are few enough: a search in
+// global memory (some trips to L2 one after another) at every new sequence cost
+// a tenth of the time at T 16384, 37 sequences (adjoint, D 1024: 112 us
+// against 84 for one sequence; 101 with the copy).  A barrier must follow.
+template <class Shared>
+__device__ __forceinline__ const int* keep_starts(Shared& sh, const int* starts, int n_seq)
+{
+    if (!starts || n_seq + 1 > kGStarts) return starts;
+    for (int i = threadIdx.x; i <= n_seq; i += blockDim.x) sh.starts[i] = __ldg(starts + i);
+    return sh.starts;
+}
 
 template <int W, int NS>
 __device__ __forceinline__ void glr_init(GlrShared<W, NS>& sh)
@@ -365,11 +380,11 @@ struct PlainRows {
     int lo = 0, hi = 0;  // first row behind the sequence's first, its last row
 };
 
-__device__ __forceinline__ RowMasks row_masks(const GlrParams& p, int t0, int rows, int lane, PlainRows& plain)
+__device__ __forceinline__ RowMasks row_masks(const GlrParams& p, const int* starts, int t0, int rows, int lane, PlainRows& plain)
 {
     RowMasks m{0u, 0u, ~0u, 0};
     if (t0 >= plain.lo && t0 + rows <= plain.hi) return m;
-    const RowSeq rs = row_seq(p.starts, p.T, p.n_seq, p.L, lane < rows ? t0 + lane : -1);
+    const RowSeq rs = row_seq(starts, p.T, p.n_seq, p.L, lane < rows ? t0 + lane : -1);
     m.firsts = __ballot_sync(0xffffffffu, rs.first);
     m.lasts = __ballot_sync(0xffffffffu, rs.last);
     m.mine = __ballot_sync(0xffffffffu, rs.owner >= 0) | (~0u << rows);
@@ -378,8 +393,8 @@ __device__ __forceinline__ RowMasks row_masks(const GlrParams& p, int t0, int ro
     const unsigned any = m.mine & ((1u << rows) - 1u);
     if (any) {
         const int o = __shfl_sync(0xffffffffu, rs.owner, 31 - __clz(any));
-        plain.lo = (p.starts ? max(__ldg(p.starts + o), 0) : o * p.L) + 1;
-        plain.hi = (p.starts ? min(__ldg(p.starts + o + 1), p.T) : (o + 1) * p.L) - 1;
+        plain.lo = (starts ? max(starts[o], 0) : o * p.L) + 1;
+        plain.hi = (starts ? min(starts[o + 1], p.T) : (o + 1) * p.L) - 1;
     }
     return m;
 }
@@ -415,6 +430,7 @@ __global__ void __launch_bounds__(GlrScanLayout<UT>::kThreads, 1) glr_scan_kerne
         if (blockIdx.x == 0) clear_outcome(p.hdr);
         glr_init(sh);
     }
+    const int* starts = keep_starts(sh, p.starts, p.n_seq);
     __syncthreads();
     bool ok = true;
     if (w >= W) {
@@ -440,7 +456,7 @@ __global__ void __launch_bounds__(GlrScanLayout<UT>::kThreads, 1) glr_scan_kerne
         // fold tile n: its rows' a and b into registers, the warp's map out
         auto fold = [&](int n, float2(&a)[R], float2(&b)[R], RowMasks& rm) {
             const int s = n % LY::kStages;
-            rm = row_masks(p, (turn + n * p.P) * LY::kTile + w * R, R, lane, plain);
+            rm = row_masks(p, starts, (turn + n * p.P) * LY::kTile + w * R, R, lane, plain);
             ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.full[s], uint32_t(n / LY::kStages) & 1u, err, p.wait_ns));
             const UT* src = reinterpret_cast<const UT*>(smem + s * LY::stage_bytes) + size_t(w) * R * 3 * kGD + 2 * lane;
             auto rows = [&](auto is_near) {
@@ -555,6 +571,7 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
         if (blockIdx.x == 0) clear_outcome(p.hdr);
         glr_init(sh);
     }
+    const int* starts = keep_starts(sh, p.starts, p.n_seq);
     __syncthreads();
     bool ok = true;
     float2 nds = both(0.f);  // minus the rates' gradients
@@ -590,7 +607,7 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
         // G = a (up + G of the row behind): the map of a row is (a, a up)
         auto fold = [&](int n, float2(&sr)[R], float2(&up)[R], RowMasks& rm) {
             const int s = n % LY::kStages;
-            rm = row_masks(p, p.T - (turn + n * p.P + 1) * LY::kTile + w * R, R, lane, plain);
+            rm = row_masks(p, starts, p.T - (turn + n * p.P + 1) * LY::kTile + w * R, R, lane, plain);
             ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.full[s], uint32_t(n / LY::kStages) & 1u, err, p.wait_ns));
             const unsigned char* stage = smem + s * LY::stage_bytes;
             const UT* su = reinterpret_cast<const UT*>(stage) + size_t(w) * R * 3 * kGD + 2 * lane;
