@@ -226,16 +226,17 @@ struct GlrShared {
     int starts[kGStarts];         // the sequences' offsets, where they fit
 };
 
-// The sequences' offsets in shared memory if there are few enough: a search in
-// global memory (some trips to L2 one after another) at every new sequence cost
-// a tenth of the time at T 16384, 37 sequences (adjoint, D 1024: 112 us
+// The sequences' offsets go to shared memory if there are few enough: a search
+// in global memory (some trips to L2 one after another) at every new sequence
+// took a tenth of the time at T 16384, 37 sequences (adjoint, D 1024: 112 us
 // against 84 for one sequence; 101 with the copy).  A barrier must follow.
+__device__ __forceinline__ bool starts_fit(int n_seq) { return n_seq + 1 <= kGStarts; }
+
 template <class Shared>
-__device__ __forceinline__ const int* keep_starts(Shared& sh, const int* starts, int n_seq)
+__device__ __forceinline__ void keep_starts(Shared& sh, const int* starts, int n_seq)
 {
-    if (!starts || n_seq + 1 > kGStarts) return starts;
+    if (!starts || !starts_fit(n_seq)) return;
     for (int i = threadIdx.x; i <= n_seq; i += blockDim.x) sh.starts[i] = __ldg(starts + i);
-    return sh.starts;
 }
 
 template <int W, int NS>
@@ -380,10 +381,11 @@ struct PlainRows {
     int lo = 0, hi = 0;  // first row behind the sequence's first, its last row
 };
 
-__device__ __forceinline__ RowMasks row_masks(const GlrParams& p, const int* starts, int t0, int rows, int lane, PlainRows& plain)
+__device__ __forceinline__ RowMasks row_masks(const GlrParams& p, const int* kept, int t0, int rows, int lane, PlainRows& plain)
 {
     RowMasks m{0u, 0u, ~0u, 0};
     if (t0 >= plain.lo && t0 + rows <= plain.hi) return m;
+    const int* starts = p.starts && starts_fit(p.n_seq) ? kept : p.starts;
     const RowSeq rs = row_seq(starts, p.T, p.n_seq, p.L, lane < rows ? t0 + lane : -1);
     m.firsts = __ballot_sync(0xffffffffu, rs.first);
     m.lasts = __ballot_sync(0xffffffffu, rs.last);
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(GlrScanLayout<UT>::kThreads, 1) glr_scan_kerne
 {
     using LY = GlrScanLayout<UT>;
     constexpr int R = LY::kRows, W = LY::kWarps, NS = LY::kSets, A_ = LY::kAhead;
-    extern __shared__ __align__(128) unsigned char smem_raw[];
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
     GlrShared<W, NS>& sh = *reinterpret_cast<GlrShared<W, NS>*>(smem + LY::kStages * LY::stage_bytes);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(GlrScanLayout<UT>::kThreads, 1) glr_scan_kerne
         if (blockIdx.x == 0) clear_outcome(p.hdr);
         glr_init(sh);
     }
-    const int* starts = keep_starts(sh, p.starts, p.n_seq);
+    keep_starts(sh, p.starts, p.n_seq);
     __syncthreads();
     bool ok = true;
     if (w >= W) {
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__(GlrScanLayout<UT>::kThreads, 1) glr_scan_kerne
         // fold tile n: its rows' a and b into registers, the warp's map out
         auto fold = [&](int n, float2(&a)[R], float2(&b)[R], RowMasks& rm) {
             const int s = n % LY::kStages;
-            rm = row_masks(p, starts, (turn + n * p.P) * LY::kTile + w * R, R, lane, plain);
+            rm = row_masks(p, sh.starts, (turn + n * p.P) * LY::kTile + w * R, R, lane, plain);
             ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.full[s], uint32_t(n / LY::kStages) & 1u, err, p.wait_ns));
             const UT* src = reinterpret_cast<const UT*>(smem + s * LY::stage_bytes) + size_t(w) * R * 3 * kGD + 2 * lane;
             auto rows = [&](auto is_near) {
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
 {
     using LY = GlrAdjointLayout<UT>;
     constexpr int R = LY::kRows, W = LY::kWarps, NS = LY::kSets, A_ = LY::kAhead;
-    extern __shared__ __align__(128) unsigned char smem_raw[];
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
     GlrShared<W, NS>& sh = *reinterpret_cast<GlrShared<W, NS>*>(smem + LY::kStages * LY::stage_bytes);
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
         if (blockIdx.x == 0) clear_outcome(p.hdr);
         glr_init(sh);
     }
-    const int* starts = keep_starts(sh, p.starts, p.n_seq);
+    keep_starts(sh, p.starts, p.n_seq);
     __syncthreads();
     bool ok = true;
     float2 nds = both(0.f);  // minus the rates' gradients
@@ -607,7 +609,7 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
         // G = a (up + G of the row behind): the map of a row is (a, a up)
         auto fold = [&](int n, float2(&sr)[R], float2(&up)[R], RowMasks& rm) {
             const int s = n % LY::kStages;
-            rm = row_masks(p, starts, p.T - (turn + n * p.P + 1) * LY::kTile + w * R, R, lane, plain);
+            rm = row_masks(p, sh.starts, p.T - (turn + n * p.P + 1) * LY::kTile + w * R, R, lane, plain);
             ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.full[s], uint32_t(n / LY::kStages) & 1u, err, p.wait_ns));
             const unsigned char* stage = smem + s * LY::stage_bytes;
             const UT* su = reinterpret_cast<const UT*>(stage) + size_t(w) * R * 3 * kGD + 2 * lane;
@@ -717,21 +719,25 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
 }
 
 // out[d] = sum of part[k][d] over k in 0..n-1, in a fixed order: 32 columns a
-// CTA, 8 interleaved runs of rows joined in order.
-__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ part, float* __restrict__ out,
-                                                         long long n, long long D)
+// CTA, 32 interleaved runs of rows (four loads of a run in flight) joined in
+// order.
+constexpr int kSumRuns = 32;
+__global__ void __launch_bounds__(32 * kSumRuns) column_sum_kernel(const float* __restrict__ part, float* __restrict__ out,
+                                                                   long long n, long long D)
 {
-    __shared__ float s[8][33];
+    __shared__ float s[kSumRuns][33];
     const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
     const long long d = (long long)blockIdx.x * 32 + c;
     float v = 0.f;
-    if (d < D)
-        for (long long k = g; k < n; k += 8) v += part[k * D + d];
+    if (d < D) {
+#pragma unroll 4
+        for (long long k = g; k < n; k += kSumRuns) v += __ldg(part + k * D + d);
+    }
     s[g][c] = v;
     __syncthreads();
     if (g == 0 && d < D) {
 #pragma unroll
-        for (int k = 1; k < 8; ++k) v += s[k][c];
+        for (int k = 1; k < kSumRuns; ++k) v += s[k][c];
         out[d] = v;
     }
 }

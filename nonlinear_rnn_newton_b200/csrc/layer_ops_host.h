@@ -179,7 +179,7 @@ pararnn_status launch_glr_adjoint(const UT* u, GlrParams p, float* drate, long l
     TRY(map_glr(&td, p.dh, PARARNN_F32, 1, p.T, D, LY::kTile));
     void* args[] = {(void*)&tu, (void*)&th, (void*)&td, (void*)&p};
     TRY(launch_glr(glr_adjoint_kernel<UT>, LY::kThreads, LY::smem_bytes, glr_layout(p.T, D, LY::kTile), &p, args, ws, st));
-    column_sum_kernel<<<unsigned((D + 31) / 32), 256, 0, st>>>(p.part, drate, p.P, D);
+    column_sum_kernel<<<unsigned((D + 31) / 32), 32 * kSumRuns, 0, st>>>(p.part, drate, p.P, D);
     return launched();
 }
 
@@ -571,7 +571,7 @@ pararnn_status pararnn_rms_norm_adjoint(const void* dy, pararnn_dtype dy_dtype, 
     else
         TRY((sum_dtype == PARARNN_BF16 ? launch_norm_adjoint<float, uint16_t>(p, s, &grid, st)
                                        : launch_norm_adjoint<float, float>(p, s, &grid, st)));
-    column_sum_kernel<<<unsigned((D + 31) / 32), 256, 0, st>>>(p.part, dw, grid, D);
+    column_sum_kernel<<<unsigned((D + 31) / 32), 32 * kSumRuns, 0, st>>>(p.part, dw, grid, D);
     return launched();
 }
 

@@ -251,9 +251,9 @@ struct NormAdjParams {
 
 // A CTA takes rows blockIdx.x * rows + k * gridDim.x * rows, and asks for its
 // next row before it works on this one; dw of its rows stays in registers and
-// leaves once, one row of `part` a CTA.  T 32768 D 2048, bf16: 98 us, 5.5 TB/s
-// (without the loads ahead 120 us); a row's two loads of three arrays by 128
-// threads, five CTAs an SM, are about 60 KB in flight on an SM.
+// leaves once, one row of `part` a CTA.  T 32768 D 2048, bf16: 94 us, 5.7 TB/s
+// (without the loads ahead 120 us, one vector a thread 108); 119 registers
+// leave four CTAs an SM, whose loads of three arrays are 48 KB in flight.
 template <class YT, class VT, int NV>
 __global__ void __launch_bounds__(kNormThreads) rms_norm_adjoint_kernel(const NormAdjParams p)
 {
