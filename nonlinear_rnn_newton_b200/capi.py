@@ -713,6 +713,10 @@ def pararnn_selftest_wait_timeout(which, limit_ns, workspace, stream=None):
 #
 # A decode step's kernels take a few microseconds, so the checks here are kept
 # to plain comparisons; _need is called to say what is wrong.
+#
+# With `stream` given, a call runs as under torch.cuda.stream(stream): what it
+# allocates (outputs, a workspace) belongs to that stream, so neither an earlier
+# nor a later use of the same memory on the current stream can meet the kernel.
 
 _CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
 _WIDE = (torch.float32, torch.bfloat16)
@@ -735,11 +739,12 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _run(fn, dev, stream, *args):
-    """Call fn(*args, stream) with `dev` current; raises unless it returns OK."""
+def _run(fn, dev, *args):
+    """Call fn(*args, the current stream of dev) with `dev` current; raises
+    unless it returns OK."""
     if dev.type != "cuda":
         raise ValueError(f"device tensors are needed, got one on {dev}")
-    raw = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    raw = torch._C._cuda_getCurrentRawStream(dev.index)
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             st = fn(*args, raw)
@@ -797,6 +802,9 @@ def pararnn_glr_scan(u, rate, h0=None, seq_starts=None, h=None, h_last=None, wan
     (r, i, x); rate [D] fp32; h0 [n_seq,D] or None.  Returns (h [B,L,D] or
     [T,D], h_last [n_seq,D] or None).  Rows in no sequence are not written: in
     an h made here they hold anything.  Asynchronous on the stream."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return pararnn_glr_scan(u, rate, h0, seq_starts, h, h_last, want_last, workspace)
     shape, T, n_seq, D = _glr_args(u, rate, h0, seq_starts)
     dev = u.device
     if h is None:
@@ -808,7 +816,7 @@ def pararnn_glr_scan(u, rate, h0=None, seq_starts=None, h=None, h_last=None, wan
     elif want_last:
         h_last = u.new_empty((n_seq, D), dtype=_f32)
     ws, at, size = _space(lib.pararnn_glr_workspace_size(T, n_seq, D), u, workspace)
-    _run(lib.pararnn_glr_scan, dev, stream, u.data_ptr(), _CODES[u.dtype], rate.data_ptr(), _address(h0),
+    _run(lib.pararnn_glr_scan, dev, u.data_ptr(), _CODES[u.dtype], rate.data_ptr(), _address(h0),
          _address(seq_starts), h.data_ptr(), _address(h_last), T, n_seq, D, at, size)
     return h, h_last
 
@@ -818,6 +826,10 @@ def pararnn_glr_adjoint(u, rate, h0, h, dh, dh_last=None, seq_starts=None, du=No
     """Gradients of pararnn_glr_scan at its states h, from dh (and dh_last or
     None).  Returns (du as u in fp32, drate [D], dh0 [n_seq,D] or None).
     Asynchronous on the stream."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return pararnn_glr_adjoint(u, rate, h0, h, dh, dh_last, seq_starts, du, drate, dh0, want_dh0,
+                                       workspace)
     shape, T, n_seq, D = _glr_args(u, rate, h0, seq_starts)
     dev = u.device
     _fits(h, "h", shape, _f32, dev)
@@ -837,7 +849,7 @@ def pararnn_glr_adjoint(u, rate, h0, h, dh, dh_last=None, seq_starts=None, du=No
     elif want_dh0:
         dh0 = u.new_empty((n_seq, D), dtype=_f32)
     ws, at, size = _space(lib.pararnn_glr_adjoint_workspace_size(T, n_seq, D), u, workspace)
-    _run(lib.pararnn_glr_adjoint, dev, stream, u.data_ptr(), _CODES[u.dtype], rate.data_ptr(), _address(h0),
+    _run(lib.pararnn_glr_adjoint, dev, u.data_ptr(), _CODES[u.dtype], rate.data_ptr(), _address(h0),
          _address(seq_starts), h.data_ptr(), dh.data_ptr(), _address(dh_last), du.data_ptr(), drate.data_ptr(),
          _address(dh0), T, n_seq, D, at, size)
     return du, drate, dh0
@@ -846,6 +858,9 @@ def pararnn_glr_adjoint(u, rate, h0, h, dh, dh_last=None, seq_starts=None, du=No
 def pararnn_glr_step(u, rate, h_prev=None, h_next=None, stream=None):
     """One step for B sequences: u [B,3,D], h_prev [B,D] (None = zeros).
     h_next may be h_prev itself (in place); a new tensor if None."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return pararnn_glr_step(u, rate, h_prev, h_next)
     if u.dim() != 3 or u.shape[1] != 3:
         raise ValueError(f"u must be [B,3,D], got shape {tuple(u.shape)}")
     B, _, D = u.shape
@@ -860,7 +875,7 @@ def pararnn_glr_step(u, rate, h_prev=None, h_next=None, stream=None):
         h_next = u.new_empty((B, D), dtype=_f32) if h_prev is None else torch.empty_like(h_prev)
     else:
         _fits(h_next, "h_next", (B, D), _f32, dev)
-    _run(lib.pararnn_glr_step, dev, stream, u.data_ptr(), code, rate.data_ptr(), _address(h_prev), h_next.data_ptr(), B,
+    _run(lib.pararnn_glr_step, dev, u.data_ptr(), code, rate.data_ptr(), _address(h_prev), h_next.data_ptr(), B,
          D)
     return h_next
 
@@ -879,6 +894,9 @@ def pararnn_rms_norm(x, w, residual=None, eps=1e-6, out_dtype=torch.bfloat16, su
     float8_e4m3fn), y_scale [..., ceil(D/128)] for 8 bits else None, sum in
     the residual's type (None without a residual), rstd [...]).  sum may be
     the residual itself (in place)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return pararnn_rms_norm(x, w, residual, eps, out_dtype, sum, y, y_scale, rstd)
     T, D = _rows(x, "x")
     dev, shape = x.device, x.shape
     yc = _code(out_dtype, "out_dtype", _CODES)
@@ -912,7 +930,7 @@ def pararnn_rms_norm(x, w, residual=None, eps=1e-6, out_dtype=torch.bfloat16, su
         rstd = x.new_empty(shape[:-1], dtype=_f32)
     else:
         _fits(rstd, "rstd", shape[:-1], _f32, dev)
-    _run(lib.pararnn_rms_norm, dev, stream, x.data_ptr(), xc, _address(residual), rc, w.data_ptr(), eps, _address(sum),
+    _run(lib.pararnn_rms_norm, dev, x.data_ptr(), xc, _address(residual), rc, w.data_ptr(), eps, _address(sum),
          y.data_ptr(), yc, _address(y_scale), rstd.data_ptr(), T, D)
     return y, y_scale, sum, rstd
 
@@ -927,6 +945,9 @@ def pararnn_rms_norm_adjoint(dy, sum, w, rstd, dsum=None, dx=None, dw=None, work
     that reaches sum from elsewhere (sum's type, or None).  Returns (dx in
     sum's type, the gradient of x and residual alike, dw [D] fp32).  dx may be
     dsum itself."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return pararnn_rms_norm_adjoint(dy, sum, w, rstd, dsum, dx, dw, workspace)
     T, D = _rows(sum, "sum")
     dev, shape = sum.device, sum.shape
     sc, yc = _code(sum.dtype, "sum", _WIDE), _code(dy.dtype, "dy", _WIDE)
@@ -946,7 +967,7 @@ def pararnn_rms_norm_adjoint(dy, sum, w, rstd, dsum=None, dx=None, dw=None, work
     else:
         _fits(dw, "dw", (D,), _f32, dev)
     ws, at, size = _space(lib.pararnn_rms_norm_adjoint_workspace_size(T, D), sum, workspace)
-    _run(lib.pararnn_rms_norm_adjoint, dev, stream, dy.data_ptr(), yc, sum.data_ptr(), sc, w.data_ptr(),
+    _run(lib.pararnn_rms_norm_adjoint, dev, dy.data_ptr(), yc, sum.data_ptr(), sc, w.data_ptr(),
          rstd.data_ptr(), _address(dsum), dx.data_ptr(), dw.data_ptr(), T, D, at, size)
     return dx, dw
 
@@ -955,6 +976,9 @@ def pararnn_fp8_quantize(x, block_rows=1, q=None, scale=None, stream=None):
     """e4m3 values of x [..., K] (bf16/fp32) and their scales: per row and 128
     columns (block_rows = 1, scale [..., ceil(K/128)]) or per 128 rows and 128
     columns (block_rows = 128, x [N,K], scale [ceil(N/128), ceil(K/128)])."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return pararnn_fp8_quantize(x, block_rows, q, scale)
     M, K = _rows(x, "x")
     dev, shape = x.device, x.shape
     xc = _code(x.dtype, "x", _WIDE)
@@ -976,7 +1000,7 @@ def pararnn_fp8_quantize(x, block_rows=1, q=None, scale=None, stream=None):
         scale = x.new_empty(blocks, dtype=_f32)
     else:
         _fits(scale, "scale", blocks, _f32, dev)
-    _run(lib.pararnn_fp8_quantize, dev, stream, x.data_ptr(), xc, block_rows, q.data_ptr(), scale.data_ptr(), M, K)
+    _run(lib.pararnn_fp8_quantize, dev, x.data_ptr(), xc, block_rows, q.data_ptr(), scale.data_ptr(), M, K)
     return q, scale
 
 
@@ -989,6 +1013,9 @@ def pararnn_fp8_project(x, x_scale, w, w_scale, bias=None, out_dtype=torch.bfloa
     """Projection of 8-bit operands: x [..., K] and w [N,K] float8_e4m3fn with
     their scales (pararnn_rms_norm or pararnn_fp8_quantize), bias [N] fp32 or
     None.  Returns u [..., N] in out_dtype (bf16 or fp32)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return pararnn_fp8_project(x, x_scale, w, w_scale, bias, out_dtype, u, workspace)
     M, K = _rows(x, "x")
     dev, shape = x.device, x.shape
     if w.dim() != 2 or w.shape[1] != K:
@@ -1006,6 +1033,6 @@ def pararnn_fp8_project(x, x_scale, w, w_scale, bias=None, out_dtype=torch.bfloa
     else:
         _fits(u, "u", shape[:-1] + (N,), out_dtype, dev)
     ws, at, size = _space(lib.pararnn_fp8_project_workspace_size(M, N, K), x, workspace)
-    _run(lib.pararnn_fp8_project, dev, stream, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
+    _run(lib.pararnn_fp8_project, dev, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
          _address(bias), u.data_ptr(), uc, M, N, K, at, size)
     return u

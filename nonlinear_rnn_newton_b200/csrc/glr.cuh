@@ -136,16 +136,25 @@ __device__ __forceinline__ RowSeq row_seq(const int* starts, int T, int n_seq, i
 constexpr int kGD = 64;        // channels of a slab
 constexpr int kGMaxP = 33;     // most CTAs of a slab
 
-// Sequences without rows: `out` gets `in` (or zeros).  The CTAs of the grid
-// share them; called by a CTA's computing threads.
+// Sequences without rows: `out` gets `in` (or zeros).  The computing warps (W a
+// CTA) of the grid share them, 32 a look.
 template <int W>
 __device__ __forceinline__ void copy_empty(const int* starts, int T, int n_seq, long long D, const float* in, float* out)
 {
     if (!starts || !out) return;
-    for (int s = blockIdx.x; s < n_seq; s += gridDim.x) {
-        const int lo = min(max(__ldg(starts + s), 0), T);
-        if (min(max(__ldg(starts + s + 1), lo), T) > lo) continue;
-        for (long long d = threadIdx.x; d < D; d += 32 * W) out[s * D + d] = in ? in[s * D + d] : 0.f;
+    const int lane = threadIdx.x & 31;
+    for (long long s0 = 32ll * (blockIdx.x * W + (threadIdx.x >> 5)); s0 < n_seq; s0 += 32ll * W * gridDim.x) {
+        bool empty = false;
+        if (s0 + lane < n_seq) {
+            const int lo = min(max(__ldg(starts + s0 + lane), 0), T);
+            empty = min(max(__ldg(starts + s0 + lane + 1), lo), T) == lo;
+        }
+        for (unsigned left = __ballot_sync(0xffffffffu, empty); left; left &= left - 1) {
+            const long long at = (s0 + __ffs(left) - 1) * D;
+            for (long long d = 4 * lane; d < D; d += 128)
+                *reinterpret_cast<float4*>(out + at + d) =
+                    in ? *reinterpret_cast<const float4*>(in + at + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
     }
 }
 

@@ -30,7 +30,8 @@ constexpr long long kNormMaxD = 8ll * kNormThreads * kNormVectors;
 constexpr float kE4m3Max = 448.0f;
 constexpr float kLeastScale = 1.17549435e-38f;  // 2^-126, the smallest normal number
 
-// eight consecutive values as loaded (16 bytes of bf16, 32 of fp32)
+// eight consecutive values as loaded (16 bytes of bf16, 32 of fp32); plain
+// loads, not those of read-only data: an output may stand in its input's place
 template <class T>
 struct Raw8;
 template <>
@@ -38,7 +39,7 @@ struct Raw8<uint16_t> {
     uint4 w;
     __device__ __forceinline__ void load(const void* p, long long i)
     {
-        w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
+        w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
     }
     __device__ __forceinline__ void get(float (&v)[8]) const
     {
@@ -56,8 +57,8 @@ struct Raw8<float> {
     __device__ __forceinline__ void load(const void* p, long long i)
     {
         const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-        a = __ldg(q);
-        b = __ldg(q + 1);
+        a = q[0];
+        b = q[1];
     }
     __device__ __forceinline__ void get(float (&v)[8]) const
     {
@@ -258,7 +259,7 @@ template <class YT, class VT, int NV>
 __global__ void __launch_bounds__(kNormThreads) rms_norm_adjoint_kernel(const NormAdjParams p)
 {
     __shared__ float s_red[2][32];
-    extern __shared__ float s_dw[];  // [rows][D] where a CTA has several rows
+    extern __shared__ __align__(16) float s_dw[];  // [rows][D] where a CTA has several rows
     const int tpr = p.tpr, rows = blockDim.x / tpr, row = threadIdx.x / tpr;
     const int lane = threadIdx.x % tpr;
     const long long D = p.D, step = (long long)gridDim.x * rows;

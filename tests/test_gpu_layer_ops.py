@@ -38,6 +38,7 @@ PACKED = [
     (64, 1500, [700, 1400]),
     (264, 40, [3, 3, 3]),                              # nothing but empty ones
     (8, 600, list(range(0, 601, 2))),                  # a start in every other row
+    (16, 900, [min(900, k // 2) for k in range(0, 2400)]),  # more than are searched in shared memory, half of them empty
 ]
 
 
@@ -489,6 +490,56 @@ def test_other_stream_and_graph(cuda):
             t.zero_()
         graph.replay()
         assert all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+def test_explicit_stream(cuda):
+    """A call on a given stream: its outputs and workspace are that stream's, so
+    work of the current stream that starts meanwhile does not meet them."""
+    B, L, D = 1, 20000, 256
+    u, rate, h0, _ = C.glr_inputs(B * L, B, D, BF16, 3)
+    ud, rd, hd = u.view(B, L, 3, D).to(cuda), rate.to(cuda), h0.to(cuda)
+    x, w = torch.randn(L, D, device=cuda), torch.ones(D, device=cuda)
+    wq, ws = P().pararnn_fp8_quantize(torch.randn(136, D, device=cuda), block_rows=128)
+    dh = torch.randn(B, L, D, device=cuda)
+
+    def run(stream):
+        y, sc, _, rstd = P().pararnn_rms_norm(x, w, out_dtype=E4M3, stream=stream)
+        q, qs = P().pararnn_fp8_quantize(x, stream=stream)
+        g = P().pararnn_fp8_project(y, sc, wq, ws, stream=stream)
+        h, last = P().pararnn_glr_scan(ud, rd, hd, stream=stream)
+        du, dr, d0 = P().pararnn_glr_adjoint(ud, rd, hd, h, dh, stream=stream)
+        dx, dw = P().pararnn_rms_norm_adjoint(x, x, w, rstd, stream=stream)
+        n = P().pararnn_glr_step(ud[:, 0].contiguous(), rd, hd, stream=stream)
+        return y.float(), sc, rstd, q.float(), qs, g, h, last, du, dr, d0, dx, dw, n
+
+    want = run(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        side.wait_stream(torch.cuda.current_stream())
+        got = run(side)
+        for n in (256, L * D * 4, 1 << 20):  # what the current stream does meanwhile
+            torch.full((n,), 255, dtype=torch.uint8, device=cuda)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        del got
+
+
+def test_outcome_is_read_from_the_workspace(cuda):
+    u, rate, h0, _ = C.glr_inputs(4000, 1, 64, BF16, 0)
+    ws = torch.full((P().pararnn_glr_adjoint_workspace_size(4000, 1, 64),), 255, dtype=torch.uint8, device=cuda)
+    ud, rd, hd = u[None].to(cuda), rate.to(cuda), h0.to(cuda)
+    h, _ = P().pararnn_glr_scan(ud, rd, hd, workspace=ws)
+    assert P().pararnn_read_result(ws)[0] == 0
+    ws.fill_(255)
+    P().pararnn_glr_adjoint(ud, rd, hd, h, h, workspace=ws)
+    assert P().pararnn_read_result(ws)[0] == 0
+    q, s = P().pararnn_fp8_quantize(torch.randn(300, 128, device=cuda))
+    wq, wsc = P().pararnn_fp8_quantize(torch.randn(136, 128, device=cuda), block_rows=128)
+    for rows in (3, 300):  # both forms of the product
+        ws.fill_(255)
+        P().pararnn_fp8_project(q[:rows], s[:rows], wq, wsc, workspace=ws[:256])
+        assert P().pararnn_read_result(ws[:256])[0] == 0
 
 
 def test_two_streams_at_once(cuda):
