@@ -754,12 +754,12 @@ def _run(fn, dev, *args):
         _check(st, allow=(OK,))
 
 
-def _space(nbytes, near, workspace):
-    """The caller's workspace or, on `near`'s device, a new one (freed in the
-    stream's order, so it lasts until the call's work is done), its address and
-    its bytes."""
+def _space(near, workspace, size, *shape):
+    """The caller's workspace or, beside the fp32 tensor `near`, a new one of
+    size(*shape) bytes (freed in the stream's order, so it lasts until the
+    call's work is done), its address and its bytes."""
     if workspace is None:
-        workspace = near.new_empty(nbytes or 256, dtype=torch.uint8)
+        workspace = near.new_empty((size(*shape) or 256) // 4)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -808,14 +808,14 @@ def pararnn_glr_scan(u, rate, h0=None, seq_starts=None, h=None, h_last=None, wan
     shape, T, n_seq, D = _glr_args(u, rate, h0, seq_starts)
     dev = u.device
     if h is None:
-        h = u.new_empty(shape, dtype=_f32)
+        h = u.new_empty(*shape, dtype=_f32)
     else:
         _fits(h, "h", shape, _f32, dev)
     if h_last is not None:
         _fits(h_last, "h_last", (n_seq, D), _f32, dev)
     elif want_last:
-        h_last = u.new_empty((n_seq, D), dtype=_f32)
-    ws, at, size = _space(lib.pararnn_glr_workspace_size(T, n_seq, D), u, workspace)
+        h_last = rate.new_empty(n_seq, D)
+    ws, at, size = _space(rate, workspace, lib.pararnn_glr_workspace_size, T, n_seq, D)
     _run(lib.pararnn_glr_scan, dev, u.data_ptr(), _CODES[u.dtype], rate.data_ptr(), _address(h0),
          _address(seq_starts), h.data_ptr(), _address(h_last), T, n_seq, D, at, size)
     return h, h_last
@@ -837,18 +837,18 @@ def pararnn_glr_adjoint(u, rate, h0, h, dh, dh_last=None, seq_starts=None, du=No
     if dh_last is not None:
         _fits(dh_last, "dh_last", (n_seq, D), _f32, dev)
     if du is None:
-        du = u.new_empty(u.shape, dtype=_f32)
+        du = torch.empty_like(u, dtype=_f32)
     else:
         _fits(du, "du", u.shape, _f32, dev)
     if drate is None:
-        drate = u.new_empty((D,), dtype=_f32)
+        drate = torch.empty_like(rate)
     else:
         _fits(drate, "drate", (D,), _f32, dev)
     if dh0 is not None:
         _fits(dh0, "dh0", (n_seq, D), _f32, dev)
     elif want_dh0:
-        dh0 = u.new_empty((n_seq, D), dtype=_f32)
-    ws, at, size = _space(lib.pararnn_glr_adjoint_workspace_size(T, n_seq, D), u, workspace)
+        dh0 = rate.new_empty(n_seq, D)
+    ws, at, size = _space(rate, workspace, lib.pararnn_glr_adjoint_workspace_size, T, n_seq, D)
     _run(lib.pararnn_glr_adjoint, dev, u.data_ptr(), _CODES[u.dtype], rate.data_ptr(), _address(h0),
          _address(seq_starts), h.data_ptr(), dh.data_ptr(), _address(dh_last), du.data_ptr(), drate.data_ptr(),
          _address(dh0), T, n_seq, D, at, size)
@@ -872,7 +872,7 @@ def pararnn_glr_step(u, rate, h_prev=None, h_next=None, stream=None):
     if h_prev is not None:
         _fits(h_prev, "h_prev", (B, D), _f32, dev)
     if h_next is None:
-        h_next = u.new_empty((B, D), dtype=_f32) if h_prev is None else torch.empty_like(h_prev)
+        h_next = rate.new_empty(B, D) if h_prev is None else torch.empty_like(h_prev)
     else:
         _fits(h_next, "h_next", (B, D), _f32, dev)
     _run(lib.pararnn_glr_step, dev, u.data_ptr(), code, rate.data_ptr(), _address(h_prev), h_next.data_ptr(), B,
@@ -909,25 +909,25 @@ def pararnn_rms_norm(x, w, residual=None, eps=1e-6, out_dtype=torch.bfloat16, su
         rc = _code(residual.dtype, "residual", _WIDE)
         _fits(residual, "residual", shape, residual.dtype, dev)
         if sum is None:
-            sum = x.new_empty(shape, dtype=residual.dtype)
+            sum = torch.empty_like(residual)
         else:
             _fits(sum, "sum", shape, residual.dtype, dev)
     elif sum is not None:
         raise ValueError("sum is an output of a call with a residual")
     if y is None:
-        y = x.new_empty(shape, dtype=out_dtype)
+        y = torch.empty_like(x, dtype=out_dtype)
     else:
         _fits(y, "y", shape, out_dtype, dev)
     if yc == E4M3:
         blocks = shape[:-1] + ((D + 127) // 128,)
         if y_scale is None:
-            y_scale = x.new_empty(blocks, dtype=_f32)
+            y_scale = w.new_empty(*blocks)
         else:
             _fits(y_scale, "y_scale", blocks, _f32, dev)
     elif y_scale is not None:
         raise ValueError("y_scale is an output of an 8-bit call")
     if rstd is None:
-        rstd = x.new_empty(shape[:-1], dtype=_f32)
+        rstd = w.new_empty(*shape[:-1])
     else:
         _fits(rstd, "rstd", shape[:-1], _f32, dev)
     _run(lib.pararnn_rms_norm, dev, x.data_ptr(), xc, _address(residual), rc, w.data_ptr(), eps, _address(sum),
@@ -959,14 +959,14 @@ def pararnn_rms_norm_adjoint(dy, sum, w, rstd, dsum=None, dx=None, dw=None, work
     if dsum is not None:
         _fits(dsum, "dsum", shape, sum.dtype, dev)
     if dx is None:
-        dx = sum.new_empty(shape, dtype=sum.dtype)
+        dx = torch.empty_like(sum)
     else:
         _fits(dx, "dx", shape, sum.dtype, dev)
     if dw is None:
-        dw = sum.new_empty((D,), dtype=_f32)
+        dw = torch.empty_like(w)
     else:
         _fits(dw, "dw", (D,), _f32, dev)
-    ws, at, size = _space(lib.pararnn_rms_norm_adjoint_workspace_size(T, D), sum, workspace)
+    ws, at, size = _space(w, workspace, lib.pararnn_rms_norm_adjoint_workspace_size, T, D)
     _run(lib.pararnn_rms_norm_adjoint, dev, dy.data_ptr(), yc, sum.data_ptr(), sc, w.data_ptr(),
          rstd.data_ptr(), _address(dsum), dx.data_ptr(), dw.data_ptr(), T, D, at, size)
     return dx, dw
@@ -993,11 +993,11 @@ def pararnn_fp8_quantize(x, block_rows=1, q=None, scale=None, stream=None):
     else:
         raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
     if q is None:
-        q = x.new_empty(shape, dtype=_e4m3)
+        q = torch.empty_like(x, dtype=_e4m3)
     else:
         _fits(q, "q", shape, _e4m3, dev)
     if scale is None:
-        scale = x.new_empty(blocks, dtype=_f32)
+        scale = x.new_empty(*blocks, dtype=_f32)
     else:
         _fits(scale, "scale", blocks, _f32, dev)
     _run(lib.pararnn_fp8_quantize, dev, x.data_ptr(), xc, block_rows, q.data_ptr(), scale.data_ptr(), M, K)
@@ -1029,10 +1029,10 @@ def pararnn_fp8_project(x, x_scale, w, w_scale, bias=None, out_dtype=torch.bfloa
     if bias is not None:
         _fits(bias, "bias", (N,), _f32, dev)
     if u is None:
-        u = x.new_empty(shape[:-1] + (N,), dtype=out_dtype)
+        u = x.new_empty(*shape[:-1], N, dtype=out_dtype)
     else:
         _fits(u, "u", shape[:-1] + (N,), out_dtype, dev)
-    ws, at, size = _space(lib.pararnn_fp8_project_workspace_size(M, N, K), x, workspace)
+    ws, at, size = _space(x_scale, workspace, lib.pararnn_fp8_project_workspace_size, M, N, K)
     _run(lib.pararnn_fp8_project, dev, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(),
          _address(bias), u.data_ptr(), uc, M, N, K, at, size)
     return u

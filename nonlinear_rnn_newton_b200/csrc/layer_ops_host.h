@@ -128,22 +128,21 @@ pararnn_status map_glr(CUtensorMap* m, const void* x, pararnn_dtype dt, int gate
     return PARARNN_OK;
 }
 
-// How many CTAs share a slab: what fits on the device at once, at most one
-// CTA a tile and kGMaxP.  They wait for one another only if there are several.
+// How many CTAs share a slab: what fits on the device at once (one an SM, by its
+// shared memory), at most one CTA a tile and kGMaxP.  They wait for one another
+// only if there are several; the launch is then a cooperative one.
 template <class K>
 pararnn_status launch_glr(K kern, int threads, size_t smem, const GlrLayout& ly, GlrParams* p, void** args, void* ws,
                           cudaStream_t st)
 {
-    int sms = 0, occ = 0;
+    int sms = 0;
     TRY(device_info(&sms));
     const void* f = reinterpret_cast<const void*>(kern);
     CUDA_TRY(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
-    CUDA_TRY(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, threads, smem));
-    if (occ < 1) return fail(PARARNN_ERR_CUDA, "kernel does not fit on an SM (smem %zu)", smem);
     unsigned char* base = static_cast<unsigned char*>(ws);
     p->S = ly.S;
     p->tiles = ly.tiles;
-    p->P = std::max(1, std::min({occ * sms / ly.S, ly.tiles, kGMaxP}));
+    p->P = std::max(1, std::min({sms / ly.S, ly.tiles, kGMaxP}));
     p->hdr = reinterpret_cast<WsHeader*>(base);
     p->maps = reinterpret_cast<uint4*>(base + ly.maps);
     p->part = reinterpret_cast<float*>(base + ly.part);
@@ -586,8 +585,14 @@ pararnn_status pararnn_fp8_quantize(const void* x, pararnn_dtype x_dtype, int bl
     if (block_rows != 1 && block_rows != 128)
         return fail(PARARNN_ERR_INVALID_ARG, "block_rows must be 1 or 128 (got %d)", block_rows);
     TRY(fp8_dims(M, 8, K));
-    const long long KB = blocks128(K), sets = block_rows == 1 ? (M * KB * 16 + 255) / 256 : blocks128(M) * KB;
-    if (sets > INT_MAX) return fail(PARARNN_ERR_INVALID_ARG, "too many blocks");
+    const long long KB = blocks128(K);
+    // rows: as many blocks of a row side by side as divide it, up to 16
+    int shift = 4;
+    while (shift < 8 && KB % (2ll << (shift - 4)) == 0) ++shift;
+    const int per = kQuantRows * (256 >> shift);
+    const dim3 rows_grid(unsigned((M + per - 1) / per), unsigned(KB >> (shift - 4)));
+    const long long sets = blocks128(M) * KB;
+    if (block_rows == 1 ? (KB >> (shift - 4)) > 65535 : sets > INT_MAX) return fail(PARARNN_ERR_INVALID_ARG, "too many blocks");
     TRY((check_apart<1, 2>({{"x", x, size_t(M) * K * dtype_bytes(x_dtype)}},
                           {{"q", q, size_t(M) * K},
                            {"scale", scale, size_t(block_rows == 1 ? M : blocks128(M)) * KB * 4}}, nullptr)));
@@ -595,11 +600,11 @@ pararnn_status pararnn_fp8_quantize(const void* x, pararnn_dtype x_dtype, int bl
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     uint8_t* out = static_cast<uint8_t*>(q);
     if (block_rows == 1) {
-        if (x_dtype == PARARNN_BF16) fp8_quantize_rows_kernel<uint16_t><<<grid, 256, 0, st>>>(x, out, scale, M, K, KB);
-        else fp8_quantize_rows_kernel<float><<<grid, 256, 0, st>>>(x, out, scale, M, K, KB);
+        if (x_dtype == PARARNN_BF16) fp8_quantize_rows_kernel<uint16_t><<<rows_grid, 256, 0, st>>>(x, out, scale, M, K, KB, shift);
+        else fp8_quantize_rows_kernel<float><<<rows_grid, 256, 0, st>>>(x, out, scale, M, K, KB, shift);
     } else {
-        if (x_dtype == PARARNN_BF16) fp8_quantize_blocks_kernel<uint16_t><<<grid, 256, 0, st>>>(x, out, scale, M, K, KB);
-        else fp8_quantize_blocks_kernel<float><<<grid, 256, 0, st>>>(x, out, scale, M, K, KB);
+        if (x_dtype == PARARNN_BF16) fp8_quantize_blocks_kernel<uint16_t><<<grid, 512, 0, st>>>(x, out, scale, M, K, KB);
+        else fp8_quantize_blocks_kernel<float><<<grid, 512, 0, st>>>(x, out, scale, M, K, KB);
     }
     return launched();
 }

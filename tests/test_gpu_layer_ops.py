@@ -340,6 +340,23 @@ def test_quantize_is_exact(cuda, M, K, rows, dtype):
     assert np.array_equal(C.f64(q.float()), O.e4m3(C.f64(z)))
 
 
+def test_quantize_is_exact_beside_the_middles(cuda):
+    """Numbers at the middle between two e4m3 values times the scale, and up to
+    six steps of fp32 to both sides of it, at scales of any mantissa: the value
+    is that of the rounded quotient, bit for bit."""
+    g = torch.Generator().manual_seed(3)
+    grid = torch.arange(0, 127, dtype=torch.uint8).view(E4M3).double()
+    middles = (grid[1:] + grid[:-1]) / 2
+    scale = (1 + torch.rand(600, generator=g)) * torch.exp2(torch.randint(-120, 118, (600,), generator=g).float())
+    x = (middles[None] * scale.double()[:, None]).float()
+    x = (x.view(torch.int32) + torch.randint(-6, 7, x.shape, generator=g, dtype=torch.int32)).view(torch.float32)
+    x = torch.cat([448 * scale[:, None], x, -x[:, :1]], 1)  # the first column sets the scale
+    want = x.abs().amax(1) / torch.tensor(448.0)
+    q, s = P().pararnn_fp8_quantize(x.contiguous().to(cuda))
+    assert x.shape[1] == 128 and torch.equal(s.cpu()[:, 0], want)
+    assert torch.equal(q.cpu().float(), (x / want[:, None]).to(E4M3).float())
+
+
 @pytest.mark.parametrize("rows", [1, 128])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_quantize_bad_values_stay_in_their_block(cuda, rows, bad):
