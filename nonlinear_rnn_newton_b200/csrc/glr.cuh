@@ -695,7 +695,8 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
                     }
                 }
             };
-            if (near && rm.plain()) run(std::true_type(), std::true_type());
+            if (__builtin_expect(near && rm.plain(), 1)) run(std::true_type(), std::true_type());
+            else if (rm.plain()) run(std::false_type(), std::true_type());
             else run(std::false_type(), std::false_type());
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.empty[s]);

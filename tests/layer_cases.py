@@ -16,11 +16,12 @@ def f64(t):
     return t.detach().cpu().double().numpy()
 
 
-def glr_inputs(T, n_seq, D, dtype, seed, starts=None):
+def glr_inputs(T, n_seq, D, dtype, seed, starts=None, fast=True):
     g = torch.Generator().manual_seed(seed)
     u = torch.randn(T, 3, D, generator=g).to(dtype)
     rate = -torch.log(0.9 + 0.099 * torch.rand(D, generator=g))
-    rate[::5] *= 40.0  # fast ones too, on both sides of the series' end
+    if fast:
+        rate[::5] *= 40.0  # fast ones too, on both sides of the series' end
     h0 = 0.5 * torch.randn(n_seq, D, generator=g)
     if starts is None:
         starts = [T // n_seq * k for k in range(n_seq + 1)]

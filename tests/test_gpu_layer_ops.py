@@ -94,6 +94,15 @@ def test_recurrence_packed(cuda, k, dtype):
     check_adjoint(cuda, u, rate, h0, starts, ud, sd, k)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D,T,starts", [(72, 700, [0, 700]), (64, 1500, [0, 1100, 1100, 1101, 1490]), PACKED[3]])
+def test_recurrence_slow_rates(cuda, D, T, starts, dtype):
+    """Every rate below 1/8: the decays come from the series alone."""
+    u, rate, h0, _ = C.glr_inputs(T, len(starts) - 1, D, dtype, seed=T, starts=starts, fast=False)
+    ud, sd, _ = check_scan(cuda, u, rate, h0, starts, True)
+    check_adjoint(cuda, u, rate, h0, starts, ud, sd, T)
+
+
 def test_recurrence_optional_arguments(cuda):
     u, rate, h0, starts = C.glr_inputs(60, 2, 16, BF16, 0)
     ud, rd = u.view(2, 30, 3, 16).to(cuda), rate.to(cuda)
