@@ -217,9 +217,8 @@ constexpr int kQThreads = 32 * (4 + kQEpi);
 constexpr int kQAhead = 4;     // blocks that a thread fetches its scales ahead
 constexpr int kQStages = 5;
 constexpr size_t kQStageBytes = size_t(kQM + kQN / 2) * kQK;
-constexpr size_t kQOut = kQStages * kQStageBytes;  // 2 x 4 KB a reading warp
-constexpr int kQOutBufs = 16 / kQEpi;
-constexpr size_t kQBar = kQOut + 16 * 4096;
+constexpr size_t kQOut = kQStages * kQStageBytes;  // 4 KB a reading warp
+constexpr size_t kQBar = kQOut + kQEpi * 4096;
 constexpr size_t kQSmem = kQBar + (2 * kQStages + 4) * 8 + 16 + 1024;
 static_assert(kQSmem <= 232448, "shared memory");
 
@@ -233,18 +232,13 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, const void* 
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// all but the last `Left` stores issued have read their shared memory
-template <int Left>
-__device__ __forceinline__ void tma_store_wait_read()
-{
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(Left) : "memory");
-}
+// the stores issued so far have read their shared memory
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
-// A warp's 32 rows x 128 columns of sums, a row a thread, to rows m0 and
-// columns n0 of u: by pieces of 128 bytes a row through 4 KB of shared memory
-// (two in turn) in the 128-byte swizzle (16-byte piece i of row r at i ^ (r %
-// 8): eight rows' writes fall in distinct banks) and a bulk store of the
-// piece.  Writing the rows from registers, 16 bytes a row and instruction,
+// A warp's 32 rows x 64 columns of sums, a row a thread, to rows m0 and columns
+// n0 of u: by pieces of 128 bytes a row through 4 KB of shared memory in the
+// 128-byte swizzle (16-byte piece i of row r at i ^ (r % 8): eight rows' writes
+// fall in distinct banks) and a bulk store of the piece.  Writing the rows from registers, 16 bytes a row and instruction,
 // took 250 of 650 us at M 32768, N 6144, K 2048.
 template <bool Bf16>
 __device__ __forceinline__ void store_sums(const Fp8Params& p, const CUtensorMap* tm_u, unsigned char* stage, int m0,
@@ -255,8 +249,7 @@ __device__ __forceinline__ void store_sums(const Fp8Params& p, const CUtensorMap
 #pragma unroll
     for (int c = 0; c < kQCols; c += kCols) {
         if (n0 + c >= p.N) break;
-        unsigned char* buf = stage + (kQOutBufs > 1 ? (c / kCols & 1) * 4096 : 0);
-        if (lane == 0) tma_store_wait_read<kQOutBufs - 1>();  // the piece that was there has left
+        if (lane == 0) tma_store_wait_read();  // the piece before has left
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -268,11 +261,11 @@ __device__ __forceinline__ void store_sums(const Fp8Params& p, const CUtensorMap
             else
                 o = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x),
                                __float_as_uint(v[1].y));
-            *reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4)) = o;
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) = o;
         }
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) tma_store_2d(tm_u, buf, n0 + c, m0);
+        if (lane == 0) tma_store_2d(tm_u, stage, n0 + c, m0);
     }
 }
 
@@ -362,7 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(112));
         const int lq = w & 3, part = (w >> 2) - 1;
         const uint32_t ta = tmem + (uint32_t(32 * lq) << 16) + uint32_t(part) * kQCols;
-        unsigned char* out = smem + kQOut + (w - 4) * 4096 * kQOutBufs;
+        unsigned char* out = smem + kQOut + (w - 4) * 4096;
         int q = 0;
         for (int t = pair; t < p.n_tiles && ok; t += pairs) {
             const int tm = t / p.tiles_n, tn = t - tm * p.tiles_n;
@@ -427,7 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
                 }
             }
         }
-        if (lane == 0) tma_store_wait_read<0>();
+        if (lane == 0) tma_store_wait_read();
     }
     if (!ok) let_copies_land();
     tc_fence_before();

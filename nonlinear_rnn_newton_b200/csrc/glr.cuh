@@ -29,6 +29,7 @@ namespace pararnn {
 // p = 1 - e^-l for l >= 0: below 1/8 from its series up to l^5 (the first term
 // left out is l^6/720, 4e-8 of the value), since 1 - ex2.approx would keep
 // only the bits of e^-l below 1: at l = 1e-3, a common decay, four digits.
+
 // Pairs of neighbouring channels: the packed fp32 instructions of this
 // architecture take both at once.
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
@@ -225,7 +226,6 @@ constexpr int kGStarts = 1025;  // offsets kept in shared memory
 constexpr int kGMaxStages = 5;
 template <int W, int NS>  // computing warps, folded tiles at a time
 struct GlrShared {
-    static constexpr int kSets = NS;
     float4 agg[NS][W][32];  // the warps' maps of the CTA's tile n, at n % NS
     float2 enter[2][W][32]; // the state entering each warp's rows, at n % 2
     int cut[NS][W];
@@ -424,10 +424,11 @@ struct GlrScanLayout {
 };
 
 template <class UT>
-__global__ void __launch_bounds__(GlrScanLayout<UT>::kThreads, 1) glr_scan_kernel(const __grid_constant__ CUtensorMap tm_u, const GlrParams p)
+__global__ void __launch_bounds__(GlrScanLayout<UT>::kThreads, 1)
+    glr_scan_kernel(const __grid_constant__ CUtensorMap tm_u, const GlrParams p)
 {
     using LY = GlrScanLayout<UT>;
-    constexpr int R = LY::kRows, W = LY::kWarps, NS = LY::kSets, A_ = LY::kAhead;
+    constexpr int R = LY::kRows, W = LY::kWarps, NS = LY::kSets, ahead = LY::kAhead;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
     GlrShared<W, NS>& sh = *reinterpret_cast<GlrShared<W, NS>*>(smem + LY::kStages * LY::stage_bytes);
@@ -530,12 +531,12 @@ __global__ void __launch_bounds__(GlrScanLayout<UT>::kThreads, 1) glr_scan_kerne
         float2 a[NS][R], b[NS][R];
         RowMasks rm[NS];
         if (mine > 0) fold(0, a[0], b[0], rm[0]);
-        if (A_ > 1 && mine > 1) fold(1, a[1], b[1], rm[1]);
+        if (ahead > 1 && mine > 1) fold(1, a[1], b[1], rm[1]);
         for (int n = 0; n < mine && ok; n += NS) {
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
                 if (n + i >= mine || !ok) break;
-                if (n + i + A_ < mine) fold(n + i + A_, a[(i + A_) % NS], b[(i + A_) % NS], rm[(i + A_) % NS]);
+                if (n + i + ahead < mine) fold(n + i + ahead, a[(i + ahead) % NS], b[(i + ahead) % NS], rm[(i + ahead) % NS]);
                 if (ok) finish(n + i, a[i], b[i], rm[i]);
             }
         }
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
                        const __grid_constant__ CUtensorMap tm_dh, const GlrParams p)
 {
     using LY = GlrAdjointLayout<UT>;
-    constexpr int R = LY::kRows, W = LY::kWarps, NS = LY::kSets, A_ = LY::kAhead;
+    constexpr int R = LY::kRows, W = LY::kWarps, NS = LY::kSets, ahead = LY::kAhead;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
     GlrShared<W, NS>& sh = *reinterpret_cast<GlrShared<W, NS>*>(smem + LY::kStages * LY::stage_bytes);
@@ -603,11 +604,11 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
             if (!ok) break;
             if (p.P > 1) glr_publish<true>(p, sh, slab, turn + n * p.P, n, lane);
             // the warps run through tile n - kAhead next, and fold tile n + 1 then
-            if (n >= A_ && n - A_ + LY::kStages < mine) {
-                const int s = (n - A_) % LY::kStages;
-                ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.empty[s], uint32_t((n - A_) / LY::kStages) & 1u, err, p.wait_ns));
+            if (n >= ahead && n - ahead + LY::kStages < mine) {
+                const int s = (n - ahead) % LY::kStages;
+                ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.empty[s], uint32_t((n - ahead) / LY::kStages) & 1u, err, p.wait_ns));
                 if (!ok) break;
-                if (lane == 0) load(n - A_ + LY::kStages);
+                if (lane == 0) load(n - ahead + LY::kStages);
             }
             ok = glr_carry<true>(p, sh, slab, turn + n * p.P, n, lane);
         }
@@ -704,12 +705,12 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
         float2 sr[NS][R], up[NS][R];
         RowMasks rm[NS];
         if (mine > 0) fold(0, sr[0], up[0], rm[0]);
-        if (A_ > 1 && mine > 1) fold(1, sr[1], up[1], rm[1]);
+        if (ahead > 1 && mine > 1) fold(1, sr[1], up[1], rm[1]);
         for (int n = 0; n < mine && ok; n += NS) {
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
                 if (n + i >= mine || !ok) break;
-                if (n + i + A_ < mine) fold(n + i + A_, sr[(i + A_) % NS], up[(i + A_) % NS], rm[(i + A_) % NS]);
+                if (n + i + ahead < mine) fold(n + i + ahead, sr[(i + ahead) % NS], up[(i + ahead) % NS], rm[(i + ahead) % NS]);
                 if (ok) finish(n + i, sr[i], up[i], rm[i]);
             }
         }
