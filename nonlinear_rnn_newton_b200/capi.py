@@ -718,8 +718,8 @@ def pararnn_selftest_wait_timeout(which, limit_ns, workspace, stream=None):
 # allocates (outputs, a workspace) belongs to that stream, so neither an earlier
 # nor a later use of the same memory on the current stream can meet the kernel.
 
-_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
-_WIDE = (torch.float32, torch.bfloat16)
+_WIDE = {torch.float32: F32, torch.bfloat16: BF16}
+_ANY = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: E4M3}
 _f32, _e4m3 = torch.float32, torch.float8_e4m3fn
 
 
@@ -729,10 +729,11 @@ def _fits(t, name, shape, dtype, device):
         _need(t, name, shape, dtype, device)
 
 
-def _code(dtype, name, allowed):
-    if dtype not in allowed:
-        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in allowed)}, got {dtype}")
-    return _CODES[dtype]
+def _code(dtype, name, codes):
+    code = codes.get(dtype)
+    if code is None:
+        raise TypeError(f"{name} must be one of {', '.join(str(d) for d in codes)}, got {dtype}")
+    return code
 
 
 def _address(t):
@@ -742,10 +743,11 @@ def _address(t):
 def _run(fn, dev, *args):
     """Call fn(*args, the current stream of dev) with `dev` current; raises
     unless it returns OK."""
-    if dev.type != "cuda":
+    index = dev.index
+    if index is None or dev.type != "cuda":
         raise ValueError(f"device tensors are needed, got one on {dev}")
-    raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    if dev.index != torch.cuda.current_device():
+    raw = torch._C._cuda_getCurrentRawStream(index)
+    if index != torch._C._cuda_getDevice():
         with torch.cuda.device(dev):
             st = fn(*args, raw)
     else:
@@ -816,7 +818,7 @@ def pararnn_glr_scan(u, rate, h0=None, seq_starts=None, h=None, h_last=None, wan
     elif want_last:
         h_last = rate.new_empty(n_seq, D)
     ws, at, size = _space(rate, workspace, lib.pararnn_glr_workspace_size, T, n_seq, D)
-    _run(lib.pararnn_glr_scan, dev, u.data_ptr(), _CODES[u.dtype], rate.data_ptr(), _address(h0),
+    _run(lib.pararnn_glr_scan, dev, u.data_ptr(), _WIDE[u.dtype], rate.data_ptr(), _address(h0),
          _address(seq_starts), h.data_ptr(), _address(h_last), T, n_seq, D, at, size)
     return h, h_last
 
@@ -849,7 +851,7 @@ def pararnn_glr_adjoint(u, rate, h0, h, dh, dh_last=None, seq_starts=None, du=No
     elif want_dh0:
         dh0 = rate.new_empty(n_seq, D)
     ws, at, size = _space(rate, workspace, lib.pararnn_glr_adjoint_workspace_size, T, n_seq, D)
-    _run(lib.pararnn_glr_adjoint, dev, u.data_ptr(), _CODES[u.dtype], rate.data_ptr(), _address(h0),
+    _run(lib.pararnn_glr_adjoint, dev, u.data_ptr(), _WIDE[u.dtype], rate.data_ptr(), _address(h0),
          _address(seq_starts), h.data_ptr(), dh.data_ptr(), _address(dh_last), du.data_ptr(), drate.data_ptr(),
          _address(dh0), T, n_seq, D, at, size)
     return du, drate, dh0
@@ -899,7 +901,7 @@ def pararnn_rms_norm(x, w, residual=None, eps=1e-6, out_dtype=torch.bfloat16, su
             return pararnn_rms_norm(x, w, residual, eps, out_dtype, sum, y, y_scale, rstd)
     T, D = _rows(x, "x")
     dev, shape = x.device, x.shape
-    yc = _code(out_dtype, "out_dtype", _CODES)
+    yc = _code(out_dtype, "out_dtype", _ANY)
     xc = _code(x.dtype, "x", _WIDE)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
