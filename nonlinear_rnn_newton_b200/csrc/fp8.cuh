@@ -137,6 +137,20 @@ __device__ __forceinline__ bool mbar_wait_clocked(uint64_t* bar, uint32_t parity
     }
 }
 
+// Self test: a wait on a barrier that nothing arrives on gives up.
+__global__ void selftest_clocked_wait_kernel(int* err, unsigned long long limit_ns)
+{
+    __shared__ uint64_t bar;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    mbar_wait_clocked(&bar, 0, err, limit_ns);
+    __syncthreads();
+    if (threadIdx.x == 0) mbar_inval(&bar);
+}
+
 // A tiled load into this CTA's shared memory that completes on a barrier of
 // either CTA of the pair (no multicast).
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* tm, int c0, int c1, uint32_t bar)

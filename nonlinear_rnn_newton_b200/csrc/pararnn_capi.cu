@@ -28,6 +28,7 @@
 #include "adjoint_ws.cuh"
 #include "linear_scan.cuh"
 #include "project.cuh"
+#include "fp8.cuh"
 
 using namespace pararnn;
 
@@ -989,7 +990,7 @@ pararnn_status linear_scan_async(const void* u, pararnn_dtype dt, const float* h
 pararnn_status selftest_wait_timeout(int which, long long limit_ns, void* ws, size_t ws_bytes, cudaStream_t stream)
 {
     t_err[0] = '\0';
-    if (which != 0 && which != 1) return fail(PARARNN_ERR_INVALID_ARG, "which must be 0 or 1");
+    if (which < 0 || which > 2) return fail(PARARNN_ERR_INVALID_ARG, "which must be 0, 1 or 2");
     if (limit_ns <= 0 || limit_ns > 10000000000ll) return fail(PARARNN_ERR_INVALID_ARG, "limit_ns out of range");
     TRY(check_workspace(ws, ws_bytes, kSelftestWorkspace));
     CUDA_TRY(cudaMemsetAsync(ws, 0, kSelftestWorkspace, stream));
@@ -999,6 +1000,9 @@ pararnn_status selftest_wait_timeout(int which, long long limit_ns, void* ws, si
     unsigned long long lim = (unsigned long long)limit_ns;
     if (which == 0) {
         selftest_lookback_kernel<<<1, 32, 0, stream>>>(desc, &hdr->error, lim);
+        CUDA_TRY(cudaGetLastError());
+    } else if (which == 2) {
+        selftest_clocked_wait_kernel<<<1, 32, 0, stream>>>(&hdr->error, lim);
         CUDA_TRY(cudaGetLastError());
     } else {
         int sms = 0;

@@ -568,6 +568,55 @@ def test_outcome_is_read_from_the_workspace(cuda):
         assert P().pararnn_read_result(ws[:256])[0] == 0
 
 
+@pytest.mark.slow
+def test_offsets_beyond_32_bits(cuda):
+    """Arrays of more than 2^31 elements: their ends are what a call on the ends
+    alone gives."""
+    T, D = 800_000, 1024  # 2.46e9 gates
+    u = torch.empty(1, T, 3, D, dtype=BF16, device=cuda)
+    for k in range(0, T, 100_000):
+        u[:, k:k + 100_000].normal_()
+    rate, dh = torch.rand(D, device=cuda) * 0.1 + 0.01, torch.randn(1, T, D, device=cuda)
+    h, last = P().pararnn_glr_scan(u, rate)
+    cut = T - 5000
+    want, wlast = P().pararnn_glr_scan(u[:, cut:].contiguous(), rate, h[:, cut - 1].contiguous())
+    # the same rows folded from other tile bounds: both within the recurrence's
+    # bound, 8 EPS of the state's envelope (below 30 here) a row over 1 / (1 - a)
+    # <= 200 rows' memory
+    assert (h[:, cut:] - want).abs().max() <= 2 * 8 * C.EPS * 30 * 200 and torch.equal(last, h[:, -1])
+    du, drate, dh0 = P().pararnn_glr_adjoint(u, rate, None, h, dh)
+    wu, _, wg = P().pararnn_glr_adjoint(u[:, cut:].contiguous(), rate, h[:, cut - 1].contiguous(),
+                                        h[:, cut:].contiguous(), dh[:, cut:].contiguous())
+    scale = wu.abs().amax((0, 1))
+    assert ((du[:, cut:] - wu).abs().amax((0, 1)) <= 1e-3 * scale).all()
+    assert torch.isfinite(du[:, :1000]).all() and torch.isfinite(drate).all() and torch.isfinite(dh0).all()
+    del du, wu, dh, want
+    flat = u.view(T * 3, D)
+    # 4000 rows: fewer are spread over more threads a row (and, in the product,
+    # over other tiles), which sums in another order; from 1184 rows of this
+    # width on the rows do not depend on how many there are
+    y, sc, _, rstd = P().pararnn_rms_norm(flat, torch.ones(D, device=cuda), out_dtype=E4M3)
+    y2, sc2, _, rstd2 = P().pararnn_rms_norm(flat[-4000:].contiguous(), torch.ones(D, device=cuda), out_dtype=E4M3)
+    assert torch.equal(y[-4000:].float(), y2.float()) and torch.equal(sc[-4000:], sc2)
+    q, qs = P().pararnn_fp8_quantize(flat)
+    q2, qs2 = P().pararnn_fp8_quantize(flat[-4000:].contiguous())
+    assert torch.equal(q[-4000:].float(), q2.float()) and torch.equal(qs[-4000:], qs2)
+    del u, flat, h, y
+    wq, ws = P().pararnn_fp8_quantize(torch.randn(1024, 1024, device=cuda), block_rows=128)
+    g = P().pararnn_fp8_project(q, qs, wq, ws)  # 2.46e9 outputs
+    assert torch.equal(g[-4000:], P().pararnn_fp8_project(q2, qs2, wq, ws))
+
+
+def test_barrier_wait_gives_up(cuda):
+    """The waits of the scans and the product end by themselves and are reported."""
+    from nonlinear_rnn_newton_b200 import capi
+    ws = torch.zeros(16384, dtype=torch.uint8, device=cuda)
+    st = capi.lib.pararnn_selftest_wait_timeout(2, 5_000_000, ws.data_ptr(), ws.numel(), None)
+    assert st == capi.ERR_TIMEOUT
+    torch.zeros(1, device=cuda).add_(1)
+    torch.cuda.synchronize()  # the context is still usable
+
+
 def test_two_streams_at_once(cuda):
     """Two recurrences at the same time, each with a workspace of its own."""
     ins = []
