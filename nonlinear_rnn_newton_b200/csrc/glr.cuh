@@ -223,15 +223,23 @@ __device__ __forceinline__ float2 apply(const Map2& m, float2 y)
 constexpr int kGStarts = 1025;  // offsets kept in shared memory
 
 // The shared parts of both scans' shared memory behind the stages.
+//
+// What lets a slot be written again: a warp folds tile n + NS, and so arrives on
+// its agg_full, only after it has run through tile n (NS = tiles ahead + 1), and
+// that needs `entered` of tile n.  So with NS slots each of agg, cut, enter and
+// their barriers, tile n + NS finds those of tile n read by every warp, without
+// a wait of its own; fewer of enter would be written while a late warp reads.
+// own and passed go between the control warps alone: the one of tile n + 2
+// waits for tile n + 1's, which comes after its look at tile n's.
 constexpr int kGMaxStages = 5;
 template <int W, int NS>  // computing warps, folded tiles at a time
 struct GlrShared {
     float4 agg[NS][W][32];  // the warps' maps of the CTA's tile n, at n % NS
-    float2 enter[2][W][32]; // the state entering each warp's rows, at n % 2
+    float2 enter[NS][W][32];  // the state entering each warp's rows, at n % NS
     int cut[NS][W];
     uint64_t full[kGMaxStages], empty[kGMaxStages];
     float2 own[2][32];            // the state that tile n ended with, at n % 2
-    uint64_t agg_full[NS], entered[2], passed[2];
+    uint64_t agg_full[NS], entered[NS], passed[2];
     int starts[kGStarts];         // the sequences' offsets, where they fit
 };
 
@@ -255,11 +263,11 @@ __device__ __forceinline__ void glr_init(GlrShared<W, NS>& sh)
         mbar_init(&sh.full[i], 1);
         mbar_init(&sh.empty[i], W);
     }
-    for (int i = 0; i < NS; ++i) mbar_init(&sh.agg_full[i], W);
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NS; ++i) {
+        mbar_init(&sh.agg_full[i], W);
         mbar_init(&sh.entered[i], 1);
-        mbar_init(&sh.passed[i], 1);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.passed[i], 1);
     fence_mbar_init();
 }
 
@@ -357,14 +365,14 @@ __device__ __forceinline__ bool glr_carry(const GlrParams& p, GlrShared<W, NS>& 
     if (cnt) own = apply(all, own);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-        sh.enter[n & 1][Reverse ? W - 1 - i : i][lane] = own;
+        sh.enter[n % NS][Reverse ? W - 1 - i : i][lane] = own;
         own = apply(warp_map<Reverse>(sh, n, i, lane), own);
     }
     sh.own[n & 1][lane] = own;
     __syncwarp();
     if (lane == 0) {
         mbar_arrive(&sh.passed[n & 1]);
-        mbar_arrive(&sh.entered[n & 1]);
+        mbar_arrive(&sh.entered[n % NS]);
     }
     return true;
 }
@@ -503,10 +511,10 @@ __global__ void __launch_bounds__(GlrScanLayout<UT>::kThreads, 1)
         };
         // run through tile n from the state entering this warp's rows
         auto finish = [&](int n, const float2(&a)[R], const float2(&b)[R], const RowMasks& rm) {
-            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.entered[n & 1], uint32_t(n >> 1) & 1u, err, p.wait_ns));
+            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.entered[n % NS], uint32_t(n / NS) & 1u, err, p.wait_ns));
             if (!ok) return;
             const int t0 = (turn + n * p.P) * LY::kTile + w * R;
-            float2 y = sh.enter[n & 1][w][lane];
+            float2 y = sh.enter[n % NS][w][lane];
             float* h = p.h + (long long)t0 * p.D + d;
             if (rm.plain()) {
 #pragma unroll
@@ -654,13 +662,13 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
             if (lane == 0) mbar_arrive(&sh.agg_full[n % NS]);
         };
         auto finish = [&](int n, const float2(&sr)[R], const float2(&up)[R], const RowMasks& rm) {
-            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.entered[n & 1], uint32_t(n >> 1) & 1u, err, p.wait_ns));
+            ok = __all_sync(0xffffffffu, mbar_wait_clocked(&sh.entered[n % NS], uint32_t(n / NS) & 1u, err, p.wait_ns));
             if (!ok) return;
             const int s = n % LY::kStages, t0 = p.T - (turn + n * p.P + 1) * LY::kTile + w * R;
             const unsigned char* stage = smem + s * LY::stage_bytes;
             const UT* su = reinterpret_cast<const UT*>(stage) + size_t(w) * R * 3 * kGD + 2 * lane;
             const float* sb = reinterpret_cast<const float*>(stage + LY::u_bytes) + w * R * kGD + 2 * lane;
-            float2 G = sh.enter[n & 1][w][lane];
+            float2 G = sh.enter[n % NS][w][lane];
             auto run = [&](auto is_near, auto is_plain) {
 #pragma unroll
                 for (int i = R - 1; i >= 0; --i) {
