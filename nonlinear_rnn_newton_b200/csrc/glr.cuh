@@ -35,25 +35,6 @@ namespace pararnn {
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 neg(float2 x) { return make_float2(-x.x, -x.y); }
 
-// a - 1 = -p from nl = -l.  Near: every rate of the warp is below 1/8, so l <=
-// rate is too and the far branch (with its special-function use) is left out.
-// Loops over rows are built for both: a branch in each row would keep the rows'
-// arithmetic from overlapping.
-template <bool Near>
-__device__ __forceinline__ float2 exp_minus_one(float2 nl)
-{
-    float2 t = __ffma2_rn(nl, both(1.0f / 120), both(1.0f / 24));
-    t = __ffma2_rn(nl, t, both(1.0f / 6));
-    t = __ffma2_rn(nl, t, both(0.5f));
-    t = __ffma2_rn(nl, t, both(1.0f));
-    t = __fmul2_rn(nl, t);
-    if constexpr (!Near) {
-        const float fx = ex2_approx(kLog2e * nl.x) - 1.0f, fy = ex2_approx(kLog2e * nl.y) - 1.0f;
-        t = make_float2(nl.x > -0.125f ? t.x : fx, nl.y > -0.125f ? t.y : fy);
-    }
-    return t;
-}
-
 __device__ __forceinline__ float2 logistic(float2 x)
 {
     const float2 y = __fmul2_rn(x, both(-kLog2e));
@@ -80,14 +61,30 @@ struct Decay2 {
     float2 nl, a, nq;
 };
 
-// nrate: the rates' negatives
+// nrate: the rates' negatives.  Near: every rate of the warp is below 1/8, so l <=
+// rate is too and the far branch (with its special-function use) is left out.
+// Loops over rows are built for both: a branch in each row would keep the rows'
+// arithmetic from overlapping.  The far branch takes a from the exponential
+// itself: 1 + (a - 1) would keep only the bits of a small a above 2^-24, and the
+// gradients of fast decays are multiples of a.
 template <bool Near>
 __device__ __forceinline__ Decay2 glr_decay(float2 sr, float2 nrate)
 {
     Decay2 g;
     g.nl = __fmul2_rn(nrate, sr);
-    const float2 np = exp_minus_one<Near>(g.nl);
+    float2 np = __ffma2_rn(g.nl, both(1.0f / 120), both(1.0f / 24));  // a - 1 = -p
+    np = __ffma2_rn(g.nl, np, both(1.0f / 6));
+    np = __ffma2_rn(g.nl, np, both(0.5f));
+    np = __ffma2_rn(g.nl, np, both(1.0f));
+    np = __fmul2_rn(g.nl, np);
     g.a = __fadd2_rn(np, both(1.0f));
+    if constexpr (!Near) {
+        const float2 y = __fmul2_rn(g.nl, both(kLog2e));
+        const float2 ex = make_float2(ex2_approx(y.x), ex2_approx(y.y)), far = __fadd2_rn(ex, both(-1.0f));
+        const bool sx = g.nl.x > -0.125f, sy = g.nl.y > -0.125f;
+        g.a = make_float2(sx ? g.a.x : ex.x, sy ? g.a.y : ex.y);
+        np = make_float2(sx ? np.x : far.x, sy ? np.y : far.y);
+    }
     g.nq = __fmul2_rn(np, __fadd2_rn(np, both(2.0f)));
     return g;
 }

@@ -44,3 +44,79 @@ def test_adjoint_repeats_bit_for_bit(cuda, D, T):
     first = P().pararnn_glr_adjoint(ud, rd, hd, h, dh)
     for _ in range(30):
         assert all(torch.equal(x, y) for x, y in zip(first, P().pararnn_glr_adjoint(ud, rd, hd, h, dh)))
+
+
+def glr_gradient_bounds(u, rate, h0, starts, h, dh, dh_last):
+    """Bounds of (du, drate, dh0) relative to the decays and to the gates'
+    slopes, in EPS, with g the larger |r| or |i| of the row:
+      e^-x: its argument x log2 e is rounded twice (the constant, the product),
+      2 |x|, and ex2's 4; s = 1 / (1 + e^-x): 2 |x| + 7; 1 - s = e^-x s: 4 |x| + 12;
+      l = rate s: 2 |x| + 8, so a = e^-l: l (2 |x| + 10) + 4, and where it is
+      1 + expm1(-l) with l < 1/8: 1 + (2 |x| + 12) / 8: both below
+      A = l (2 g + 10) + g / 4 + 4;
+      1 - a: a A / (1 - a) + 1, where a l / (1 - a) <= 1 and (l >= 1/8) a / (1 - a)
+      <= 7.6: below 4 g + 45 (series: 2 g + 13); 1 - a^2: 4 more; m and 1 / m: half
+      of that and 6: Q = 2 g + 31.
+    lam adds up and is multiplied by a: A and 4 for the maps a row.  The outputs
+    multiply lam, s(i), x, m or 1 / m, a^2 (2 A), h, l and 1 - s: their own factors'
+    errors and 2 a product."""
+    a, m, sr, si, x, left = O.glr_coefficients(u, rate)
+    T, _, D = u.shape
+    g = np.maximum(np.abs(u[:, 0]), np.abs(u[:, 1]))
+    A, Q = left * (2 * g + 10) + g / 4 + 4, 2 * g + 31
+    not_r, not_i = O.sigmoid(-u[:, 0]), O.sigmoid(-u[:, 1])
+    du, drate, dh0 = np.zeros((T, 3, D)), np.zeros(D), np.zeros_like(dh_last)
+    size, rows = np.zeros(D), 0
+    for s in range(len(starts) - 1):
+        lo, hi = starts[s], starts[s + 1]
+        e, env = np.zeros(D), np.abs(dh_last[s])
+        for t in range(hi - 1, lo - 1, -1):
+            env = env + np.abs(dh[t])
+            e = e + 3 * C.EPS * env
+            before = np.abs(h0[s] if t == lo else h[t - 1])
+            into = si[t] * np.abs(x[t]) * a[t] ** 2 / m[t] + a[t] * before
+            fresh = m[t] * si[t]
+            dl = into * (e + (2 * A[t] + Q[t] + 2 * g[t] + 17) * C.EPS * env)
+            du[t, 0] = left[t] * not_r[t] * (dl + into * (6 * g[t] + 26) * C.EPS * env)
+            du[t, 2] = fresh * (e + (Q[t] + 2 * g[t] + 13) * C.EPS * env)
+            du[t, 1] = np.abs(x[t]) * not_i[t] * (du[t, 2] + fresh * (4 * g[t] + 16) * C.EPS * env)
+            drate += sr[t] * (dl + into * (2 * g[t] + 9) * C.EPS * env)
+            size += into * sr[t] * env
+            rows += 1
+            e = a[t] * (e + (A[t] + 5) * C.EPS * env)
+            env = a[t] * env
+        dh0[s] = e
+    return du + 1e-36, drate + rows * C.EPS * size + 1e-36, dh0 + 1e-36
+
+
+def check_gradients(dev, u, rate, h0, starts, seed):
+    T, _, D = u.shape
+    g = torch.Generator().manual_seed(seed)
+    h, dh = torch.randn(T, D, generator=g), torch.randn(T, D, generator=g)
+    dl = torch.randn(len(starts) - 1, D, generator=g)
+    sd = torch.tensor(starts, dtype=torch.int32, device=dev)
+    got = P().pararnn_glr_adjoint(u.to(dev), rate.to(dev), h0.to(dev), h.to(dev), dh.to(dev), dh_last=dl.to(dev),
+                                  seq_starts=sd)
+    args = [C.f64(t) for t in (u, rate, h0)] + [starts] + [C.f64(t) for t in (h, dh, dl)]
+    du, drate, dh0, _ = O.glr_adjoint(*args)
+    # the oracle's 1 - s is a difference: from the logistic of -x it keeps its digits
+    for k in range(2):
+        s = O.sigmoid(args[0][:, k])
+        with np.errstate(divide="ignore", invalid="ignore"):
+            du[:, k] = np.where(s < 1, du[:, k] / (1 - s), 0) * O.sigmoid(-args[0][:, k])
+    bounds = glr_gradient_bounds(*args)
+    for name, x, y, b in zip(("du", "drate", "dh0"), got, (du, drate, dh0), bounds):
+        near(x, y, b, name)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("starts", [[0, 200], [0, 1, 2, 90, 200]], ids=["one", "several"])
+def test_gradients_of_fast_decays(cuda, starts, dtype):
+    """Decays down to e^-28: what is multiplied by a keeps a's own digits."""
+    T, D = 200, 72
+    g = torch.Generator().manual_seed(21)
+    u = torch.randn(T, 3, D, generator=g).to(dtype)
+    u[:, :2] = u[:, :2].clamp(-2.5, 2.5)
+    rate = torch.tensor([0.05, 0.2, 1.0, 3.0, 6.0, 10.0, 15.0, 20.0, 30.0]).repeat(8)
+    h0 = torch.randn(len(starts) - 1, D, generator=g)
+    check_gradients(cuda, u, rate, h0, starts, 22)
