@@ -560,8 +560,9 @@ PARARNN_API pararnn_status pararnn_glr_step(const void* u, pararnn_dtype u_dtype
  *   y        [T][D] y_dtype out: fp32, bf16 or e4m3
  *   y_scale  [T][ceil(D/128)] fp32 out for e4m3 (else ignored): per row and
  *            block of 128 columns max(largest |y| / 448, 2^-126);
- *            y ~ e4m3 value x scale.  A block that holds NaN or infinity
- *            stands for NaN throughout.
+ *            y ~ e4m3 value x scale, the bits that pararnn_fp8_quantize
+ *            makes of an fp32 y.  A block that holds NaN or infinity stands
+ *            for NaN throughout.
  *   rstd     [T] fp32 out for the adjoint, or NULL
  * y and the scales come from the unrounded v.  D a multiple of 8 (16 for
  * e4m3) and at most 16384, else UNSUPPORTED.  Other overlaps of outputs are

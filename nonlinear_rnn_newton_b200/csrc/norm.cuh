@@ -4,7 +4,7 @@
 //   v = x + residual,  sum = v in the residual's type,
 //   rstd = 1 / sqrt(mean(v^2) + eps),  y = v rstd w;
 //   8 bits: per block of 128 columns scale = max(amax / 448, 2^-126) and
-//   q = e4m3(y / scale).
+//   q = e4m3(y / scale), the same bits that the quantiser makes of an fp32 y.
 // Adjoint, with n = v rstd and g = dy w:
 //   dx = dsum + rstd (g - n mean(g n)),  dw = sum over rows of dy n.
 //
@@ -12,8 +12,9 @@
 // vector, NV vectors a thread) and everything else happens there.  A row
 // belongs to `tpr` threads (a multiple of 32); 16 neighbouring lanes hold one
 // block of 128 columns, so its scale needs four shuffles.  The norm of T 32768
-// D 2048 (fp32 in, bf16 residual, e4m3 out) takes 92 us, 6.5 TB/s, as much as a
-// copy.
+// D 2048 (fp32 in, bf16 residual, e4m3 out) takes 98 to 100 us, 6.1 TB/s: 96 with
+// a product by the scale's rounded reciprocal for the quotient, which puts
+// values beside a middle on its other side.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -144,6 +145,31 @@ __device__ __forceinline__ float max16(float m)
     return m;
 }
 
+// v / sc rounded to fp32, for the norm and the quantiser: bf16 values often lie
+// halfway between two e4m3 ones, and the rounded quotient then decides, so a
+// product with 1 / sc alone will not do.  Markstein's correction (P. Markstein, "Computation of elementary functions
+// on the IBM RISC System/6000", 1990): with y = 1 / sc rounded and q = v y, the
+// residual v - q sc is exact in one fused multiply-add, and q + residual y
+// rounds to the quotient.  The residual must not underflow, so small blocks are
+// scaled up by 2^64 first, which is exact.  Tested bit for bit against IEEE
+// division.  The quantiser, M 16384 K 4096, bf16: 41 us (4.9 TB/s; fp32 51, 6.6 TB/s); with a
+// division each 55; a reciprocal with divisions only beside the middles 81, for
+// its branches.
+__device__ __forceinline__ P8 quotients(const P8& v, float sc)
+{
+    const float up = sc < 1e-25f ? 18446744073709551616.0f : 1.0f;
+    const float s = sc * up;
+    const float2 y = twice(1.0f / s), ns = twice(-s);
+    P8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = __fmul2_rn(v.v[i], twice(up));
+        const float2 q = __fmul2_rn(x, y);
+        r.v[i] = __ffma2_rn(__ffma2_rn(q, ns, x), y, q);
+    }
+    return r;
+}
+
 // Sum of v over the tpr threads of this row; every thread gets it.  s: one
 // float per warp of the CTA.  Every thread of the CTA calls it.
 __device__ __forceinline__ float row_sum(float v, int tpr, float* s)
@@ -225,13 +251,8 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormParams
         for (int j = 0; j < 4; ++j) y.v[j] = in ? __fmul2_rn(__fmul2_rn(v[k].v[j], twice(rstd)), y.v[j]) : twice(0.f);
         if (p.y_dtype == PARARNN_E4M3) {
             const float sc = scale_of(max16(amax8(y)));
-            // one reciprocal a block: a division for each value took as long
-            // as the memory (T 32768 D 2048: 122 us)
-            const float2 inv = twice(1.0f / sc);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y.v[j] = __fmul2_rn(y.v[j], inv);
             if (in) {
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + base + c) = pack_e4m3x8(y);
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + base + c) = pack_e4m3x8(quotients(y, sc));
                 if ((lane & 15) == 0) p.scale[t * ((D + 127) / 128) + c / 128] = sc;
             }
         } else if (in) {
@@ -352,31 +373,6 @@ __global__ void __launch_bounds__(kNormThreads) rms_norm_adjoint_kernel(const No
 }
 
 // ------------------------------------------------------- 8-bit quantisation
-
-// v / sc rounded to fp32: bf16 values often lie halfway between two e4m3 ones,
-// and the rounded quotient then decides, so a product with 1 / sc alone will not
-// do.  Markstein's correction (P. Markstein, "Computation of elementary functions
-// on the IBM RISC System/6000", 1990): with y = 1 / sc rounded and q = v y, the
-// residual v - q sc is exact in one fused multiply-add, and q + residual y
-// rounds to the quotient.  The residual must not underflow, so small blocks are
-// scaled up by 2^64 first, which is exact.  Tested bit for bit against IEEE
-// division.  M 16384 K 4096, bf16: 41 us (4.9 TB/s; fp32 51, 6.6 TB/s); with a
-// division each 55; a reciprocal with divisions only beside the middles 81, for
-// its branches.
-__device__ __forceinline__ P8 quotients(const P8& v, float sc)
-{
-    const float up = sc < 1e-25f ? 18446744073709551616.0f : 1.0f;
-    const float s = sc * up;
-    const float2 y = twice(1.0f / s), ns = twice(-s);
-    P8 r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 x = __fmul2_rn(v.v[i], twice(up));
-        const float2 q = __fmul2_rn(x, y);
-        r.v[i] = __ffma2_rn(__ffma2_rn(q, ns, x), y, q);
-    }
-    return r;
-}
 
 // One scale per row and 128 columns: 16 lanes a block, 8 columns a lane.  A CTA
 // takes 2^shift vectors of 8 columns of kQuantRows times 256 / 2^shift rows, so

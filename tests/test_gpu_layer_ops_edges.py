@@ -120,3 +120,20 @@ def test_gradients_of_fast_decays(cuda, starts, dtype):
     rate = torch.tensor([0.05, 0.2, 1.0, 3.0, 6.0, 10.0, 15.0, 20.0, 30.0]).repeat(8)
     h0 = torch.randn(len(starts) - 1, D, generator=g)
     check_gradients(cuda, u, rate, h0, starts, 22)
+
+
+@pytest.mark.parametrize("T,D", [(1, 16), (3, 128), (50, 1040), (9, 2048), (5, 4112), (2, 16384), (1000, 512)])
+@pytest.mark.parametrize("x,res", [(F32, BF16), (BF16, BF16), (BF16, None), (F32, F32)],
+                         ids=lambda t: "none" if t is None else str(t)[6:])
+def test_norm_in_8_bits_is_the_norm_quantised(cuda, T, D, x, res):
+    """The 8-bit output is what the quantiser makes of the fp32 output, bit for
+    bit: the rounded quotient by the scale decides."""
+    g = torch.Generator().manual_seed(T + D)
+    xs = torch.randn(T, D, generator=g).to(x).to(cuda)
+    rs = None if res is None else (2 * torch.randn(T, D, generator=g)).to(res).to(cuda)
+    w = (1 + 0.1 * torch.randn(D, generator=g)).to(cuda)
+    y, scale, _, _ = P().pararnn_rms_norm(xs, w, residual=rs, out_dtype=E4M3)
+    wide, _, _, _ = P().pararnn_rms_norm(xs, w, residual=rs, out_dtype=F32)
+    q, s = P().pararnn_fp8_quantize(wide)
+    assert torch.equal(scale, s)
+    assert torch.equal(y.view(torch.uint8), q.view(torch.uint8))
