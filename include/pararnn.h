@@ -609,7 +609,10 @@ PARARNN_API pararnn_status pararnn_fp8_quantize(const void* x, pararnn_dtype x_d
  *   u[m][n] = sum over blocks b of 128 columns of
  *             x_scale[m][b] w_scale[n / 128][b] (x[m] . w[n] over block b)
  *             + bias[n],
- * each block's product and the sum over blocks in fp32, rounded once.
+ * each block's product and the sum over blocks in fp32, rounded once.  The
+ * two scales of a block are multiplied first, in fp32: where their product is
+ * below 2^-126 the block's term is off by up to 2^-125 (nothing but sums below
+ * 1e-30 or so can tell), and it must not exceed fp32's largest number.
  *   x       [M][K] e4m3, x_scale [M][ceil(K/128)] fp32 (pararnn_rms_norm, or
  *           pararnn_fp8_quantize with block_rows 1)
  *   w       [N][K] e4m3, w_scale [ceil(N/128)][ceil(K/128)] fp32

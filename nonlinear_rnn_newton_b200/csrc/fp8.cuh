@@ -7,7 +7,11 @@
 // The tensor cores (tcgen05, kind::f8f6f4) form each block's product on its
 // own: the scales are any fp32 numbers, so a block's accumulator leaves
 // tensor memory before the next block's scale can join, and the sum over
-// blocks is kept in registers, acc += (xs ws) t.  Two accumulators in tensor
+// blocks is kept in registers, acc += (xs ws) t.  xs ws is rounded to fp32 first.
+// Where it is below 2^-126 that is off by up to 2^-150, and the term by 2^-125 (a
+// block's sum is below 2^25); the interface says so.  Taking such a block's two
+// factors one after the other, behind a vote of the warp, cost M 32768 N 6144
+// K 2048 8 % (442 -> 477 us), and 39 % where half of the rows are zeros.  Two accumulators in tensor
 // memory let the next block's product run while this one is read.
 //
 // A block is one 128-byte row of the 128-byte swizzle: a stage holds one

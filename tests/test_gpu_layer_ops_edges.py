@@ -137,3 +137,26 @@ def test_norm_in_8_bits_is_the_norm_quantised(cuda, T, D, x, res):
     q, s = P().pararnn_fp8_quantize(wide)
     assert torch.equal(scale, s)
     assert torch.equal(y.view(torch.uint8), q.view(torch.uint8))
+
+
+@pytest.mark.parametrize("M", [5, 40, 100, 300, 1000])
+@pytest.mark.parametrize("total", [-20, -118, -142, -155])
+def test_project_of_small_scales(cuda, M, total):
+    """Scales from 2^-115 to 2^115 whose product is about 2^total, however the
+    exponent is split: exact to fp32 while the product is a normal number, and
+    off by 2^-125 a block at most where it is not."""
+    N, K = 264, 1104
+    KB = (K + 127) // 128
+    g = torch.Generator().manual_seed(M)
+    x = (64 * torch.randn(M, K, generator=g)).clamp(-448, 448).to(E4M3)
+    w = (64 * torch.randn(N, K, generator=g)).clamp(-448, 448).to(E4M3)
+    split = torch.linspace(-115, total + 115, KB).round()
+    xs = torch.exp2(split).repeat(M, 1) * (0.5 + torch.rand(M, KB, generator=g))
+    ws = torch.exp2(total - split).repeat((N + 127) // 128, 1) * (0.5 + torch.rand((N + 127) // 128, KB, generator=g))
+    got = P().pararnn_fp8_project(x.to(cuda), xs.to(cuda), w.to(cuda), ws.to(cuda), out_dtype=F32)
+    want, size = O.fp8_project(C.f64(x.float()), C.f64(xs), C.f64(w.float()), C.f64(ws), None)
+    # a block's 128 products, the blocks' terms and sums; the products of scales
+    # are 1/4 to 9/4 of 2^total
+    rel = (2 * 128 + 4 * KB + 4) * C.EPS
+    small = KB * 2.0 ** -125 if total < -124 else 0.0
+    near(got, want, rel * size + 2 * C.EPS * np.abs(want) + small, "u")
