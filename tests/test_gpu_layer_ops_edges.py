@@ -98,12 +98,14 @@ def check_gradients(dev, u, rate, h0, starts, seed):
     got = P().pararnn_glr_adjoint(u.to(dev), rate.to(dev), h0.to(dev), h.to(dev), dh.to(dev), dh_last=dl.to(dev),
                                   seq_starts=sd)
     args = [C.f64(t) for t in (u, rate, h0)] + [starts] + [C.f64(t) for t in (h, dh, dl)]
-    du, drate, dh0, _ = O.glr_adjoint(*args)
-    # the oracle's 1 - s is a difference: from the logistic of -x it keeps its digits
-    for k in range(2):
-        s = O.sigmoid(args[0][:, k])
-        with np.errstate(divide="ignore", invalid="ignore"):
-            du[:, k] = np.where(s < 1, du[:, k] / (1 - s), 0) * O.sigmoid(-args[0][:, k])
+    du, drate, dh0, lam = O.glr_adjoint(*args)
+    # the oracle's 1 - s is a difference, 0 from x = 37 on: the logistic of -x keeps its digits
+    a, m, _, si, x, left = O.glr_coefficients(*args[:2])
+    before = np.concatenate([args[4][:1], args[4][:-1]])
+    for s, first in enumerate(starts[:-1]):
+        before[first] = args[2][s]
+    du[:, 0] = lam * (si * x * a * a / m - a * before) * left * O.sigmoid(-args[0][:, 0])
+    du[:, 1] = lam * m * x * si * O.sigmoid(-args[0][:, 1])
     bounds = glr_gradient_bounds(*args)
     for name, x, y, b in zip(("du", "drate", "dh0"), got, (du, drate, dh0), bounds):
         near(x, y, b, name)
@@ -160,3 +162,26 @@ def test_project_of_small_scales(cuda, M, total):
     rel = (2 * 128 + 4 * KB + 4) * C.EPS
     small = KB * 2.0 ** -125 if total < -124 else 0.0
     near(got, want, rel * size + 2 * C.EPS * np.abs(want) + small, "u")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("slow", [True, False], ids=["slow", "fast"])
+def test_gradients_of_saturated_gates(cuda, slow, dtype):
+    """Gates from -50 to 50.  1 - s is a difference, so dr and di keep the
+    absolute error that they have at an open gate: the bounds of layer_cases
+    take 1 - s as 1, and s(x) of |x| <= 50 has up to 2 50 + 7 EPS where theirs
+    of |x| <= 8 has up to 23, hence five times these."""
+    T, D = 130, 72
+    g = torch.Generator().manual_seed(31)
+    u = torch.randn(T, 3, D, generator=g)
+    u[:, :2] = 100 * torch.rand(T, 2, D, generator=g) - 50
+    u = u.to(dtype)
+    rate = (0.001 + 0.12 * torch.rand(D, generator=g)) * (1 if slow else 20)
+    h0, dl = torch.randn(1, D, generator=g), torch.randn(1, D, generator=g)
+    h, dh = torch.randn(1, T, D, generator=g), torch.randn(1, T, D, generator=g)
+    got = P().pararnn_glr_adjoint(u[None].to(cuda), rate.to(cuda), h0.to(cuda), h.to(cuda), dh.to(cuda),
+                                  dh_last=dl.to(cuda))
+    args = [C.f64(t) for t in (u, rate, h0)] + [[0, T]] + [C.f64(t) for t in (h[0], dh[0], dl)]
+    want = O.glr_adjoint(*args)
+    for name, x, y, b in zip(("du", "drate", "dh0"), got, want, C.glr_adjoint_bounds(*args)):
+        near(x.view(y.shape), y, 5 * b, name)
