@@ -591,7 +591,12 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
     keep_starts(sh, p.starts, p.n_seq);
     __syncthreads();
     bool ok = true;
-    float2 nds = both(0.f);  // minus the rates' gradients
+    // Minus the rates' gradients: sums of terms of either sign over all of the
+    // thread's rows, one or two thousand.  A tile's rows are added up, then joined
+    // by compensated summation (W. Kahan, "Further remarks on reducing truncation
+    // errors", 1965): 2 EPS of the terms' magnitudes however many there are.  The
+    // warps' and the CTAs' sums, 10 and 33 at most, are then added plainly.
+    float2 nds = both(0.f), rest = both(0.f);
     if (w >= W) {
         auto load = [&](int n) {
             const int s = n % LY::kStages, t = p.T - (turn + n * p.P + 1) * LY::kTile;
@@ -665,7 +670,7 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
             const unsigned char* stage = smem + s * LY::stage_bytes;
             const UT* su = reinterpret_cast<const UT*>(stage) + size_t(w) * R * 3 * kGD + 2 * lane;
             const float* sb = reinterpret_cast<const float*>(stage + LY::u_bytes) + w * R * kGD + 2 * lane;
-            float2 G = sh.enter[n % NS][w][lane];
+            float2 G = sh.enter[n % NS][w][lane], tile_nds = both(0.f);
             auto run = [&](auto is_near, auto is_plain) {
 #pragma unroll
                 for (int i = R - 1; i >= 0; --i) {
@@ -688,7 +693,7 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
                     // dl = lam (s(i) x a^2 / m - a h), negated
                     const float2 ndl = __ffma2_rn(G, before, __fmul2_rn(__fmul2_rn(lx, __fmul2_rn(g.a, g.a)), nim));
                     const float2 dr = __fmul2_rn(__fmul2_rn(ndl, g.nl), __ffma2_rn(sr[i], both(-1.f), both(1.f)));
-                    nds = __ffma2_rn(ndl, sr[i], nds);
+                    tile_nds = __ffma2_rn(ndl, sr[i], tile_nds);
                     if (in) {
                         float* q = p.du + (long long)(t0 + i) * 3 * p.D + d;
                         *reinterpret_cast<float2*>(q) = dr;
@@ -706,6 +711,9 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
             else run(std::false_type(), std::false_type());
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.empty[s]);
+            const float2 y = __fadd2_rn(tile_nds, neg(rest)), all = __fadd2_rn(nds, y);
+            rest = __fadd2_rn(__fadd2_rn(all, neg(nds)), neg(y));
+            nds = all;
         };
         float2 sr[NS][R], up[NS][R];
         RowMasks rm[NS];

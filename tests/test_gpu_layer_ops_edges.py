@@ -185,3 +185,21 @@ def test_gradients_of_saturated_gates(cuda, slow, dtype):
     want = O.glr_adjoint(*args)
     for name, x, y, b in zip(("du", "drate", "dh0"), got, want, C.glr_adjoint_bounds(*args)):
         near(x.view(y.shape), y, 5 * b, name)
+
+
+def test_rate_gradient_of_many_equal_rows(cuda):
+    """Every row adds the same to drate, so roundings of a running sum would
+    all fall to one side: -s(r) a row, T times.  s(r) has the logistic's error;
+    a thread's sum 2 EPS, then ten warps' and 33 CTAs' at most are added."""
+    T, D = 8000, 4800  # 800 rows a thread
+    g = torch.Generator().manual_seed(0)
+    r = torch.randn(D, generator=g).clamp(-4, 4).to(BF16)
+    u = torch.zeros(1, T, 3, D, dtype=BF16, device=cuda)
+    u[:, :, 0] = r.to(cuda)
+    one = torch.ones(1, T, D, device=cuda)
+    # no decay: lam = 1 and h = 1 in every row
+    _, drate, dh0 = P().pararnn_glr_adjoint(u, torch.zeros(D, device=cuda), one[:, 0].contiguous(), one,
+                                            torch.zeros_like(one), dh_last=one[:, 0].contiguous())
+    assert torch.equal(dh0, one[:, 0])
+    want = -T * O.sigmoid(C.f64(r))
+    near(drate, want, (2 * np.abs(C.f64(r)) + 7 + 2 + 43) * C.EPS * np.abs(want), "drate")
