@@ -762,6 +762,8 @@ def _space(near, workspace, size, *shape):
     call's work is done), its address and its bytes."""
     if workspace is None:
         workspace = near.new_empty((size(*shape) or 256) // 4)
+    elif workspace.device != near.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {near.device}, is on {workspace.device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

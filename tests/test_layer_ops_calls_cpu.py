@@ -1,0 +1,49 @@
+"""Calls of the layer operators that the C entry points or the binding refuse:
+workspaces and streams that are not the call's.  No GPU is needed: every refusal
+comes before a device call."""
+import types
+
+import pytest
+import torch
+
+A = [1 << 20 << k for k in range(14)]  # fake pointers, far apart
+
+
+@pytest.fixture(scope="module")
+def capi():
+    from nonlinear_rnn_newton_b200 import build
+    build.build()
+    from nonlinear_rnn_newton_b200 import capi
+    return capi
+
+
+def calls(P):
+    """Each operator on small arguments; kw goes to the call."""
+    u, rate = torch.zeros(2, 3, 3, 16), torch.zeros(16)
+    h, x, r = torch.zeros(2, 3, 16), torch.zeros(4, 32), torch.ones(4)
+    q, s = torch.zeros(4, 32).to(torch.float8_e4m3fn), torch.ones(4, 1)
+    w, ws = torch.zeros(8, 32).to(torch.float8_e4m3fn), torch.ones(1, 1)
+    with_workspace = [
+        lambda **kw: P.pararnn_glr_scan(u, rate, **kw),
+        lambda **kw: P.pararnn_glr_adjoint(u, rate, None, h, h, **kw),
+        lambda **kw: P.pararnn_rms_norm_adjoint(x, x, torch.ones(32), r, **kw),
+        lambda **kw: P.pararnn_fp8_project(q, s, w, ws, **kw),
+    ]
+    others = [
+        lambda **kw: P.pararnn_glr_step(torch.zeros(2, 3, 16), rate, **kw),
+        lambda **kw: P.pararnn_rms_norm(x, torch.ones(32), **kw),
+        lambda **kw: P.pararnn_fp8_quantize(x, **kw),
+    ]
+    return with_workspace, others
+
+
+def test_workspace_of_another_device(capi):
+    for call in calls(capi)[0]:
+        with pytest.raises(ValueError, match="workspace"):
+            call(workspace=torch.empty(1 << 16, dtype=torch.uint8, device="meta"))
+
+
+def test_workspace_with_gaps(capi):
+    for call in calls(capi)[0]:
+        with pytest.raises(ValueError, match="workspace"):
+            call(workspace=torch.empty(2, 1 << 16, dtype=torch.uint8)[:, ::2])
