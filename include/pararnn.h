@@ -511,9 +511,10 @@ PARARNN_API pararnn_status pararnn_lstm_step(const void* u, pararnn_dtype u_dtyp
  *              is empty), which glr_step continues from; or NULL
  * A sequence's result does not depend on what the others hold, NaN and
  * infinities included.  4-byte alignment suffices for seq_starts.  Outputs
- * must not overlap inputs or each other.  Asynchronous on `stream`,
- * capturable in a CUDA graph; a device-side failure (a bounded wait that ran
- * out) is reported by pararnn_read_result on the same workspace.  Calls that
+ * and workspaces, here and below, must not overlap inputs or each other.
+ * Asynchronous on `stream`, capturable in a CUDA graph; a device-side failure
+ * (a bounded wait that ran out) is reported by pararnn_read_result on the same
+ * workspace.  Calls that
  * may run at the same time need workspaces of their own. */
 PARARNN_API size_t pararnn_glr_workspace_size(int64_t T, int64_t n_seq, int64_t D);
 PARARNN_API pararnn_status pararnn_glr_scan(const void* u, pararnn_dtype u_dtype, const float* rate,

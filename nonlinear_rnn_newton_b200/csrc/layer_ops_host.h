@@ -35,11 +35,18 @@ struct Range {
     size_t bytes;
 };
 
-// no output may meet an input or another output; {in, out} pairs for which
-// `out` may be the very buffer of `in` are listed as equal pointers allowed
+// no output (nor the workspace, where there is one) may meet an input or another
+// output; `in_place`: where an output may be the very buffer of an input
 template <int NI, int NO>
-pararnn_status check_apart(const Range (&in)[NI], const Range (&out)[NO], const void* in_place)
+pararnn_status check_apart(const Range (&in)[NI], const Range (&out)[NO], const void* in_place,
+                           const Range& space = Range{"workspace", nullptr, 0})
 {
+    for (int j = 0; j < NI; ++j)
+        if (meet(in[j].p, in[j].bytes, space.p, space.bytes))
+            return fail(PARARNN_ERR_INVALID_ARG, "workspace overlaps input %s", in[j].name);
+    for (int j = 0; j < NO; ++j)
+        if (meet(out[j].p, out[j].bytes, space.p, space.bytes))
+            return fail(PARARNN_ERR_INVALID_ARG, "workspace overlaps output %s", out[j].name);
     for (int i = 0; i < NO; ++i) {
         for (int j = 0; j < NI; ++j)
             if (meet(in[j].p, in[j].bytes, out[i].p, out[i].bytes) &&
@@ -388,10 +395,11 @@ pararnn_status pararnn_glr_scan(const void* u, pararnn_dtype u_dtype, const floa
     TRY(check_ptr(h_last, "h_last", false));
     TRY(glr_shape(T, n_seq, D, seq_starts));
     const size_t rows = size_t(T) * D, ends = size_t(n_seq) * D * 4;
+    const size_t need = glr_ws_bytes(false, T, n_seq, D);
     TRY((check_apart<4, 2>({{"u", u, rows * 3 * dtype_bytes(u_dtype)}, {"rate", rate, size_t(D) * 4}, {"h0", h0, ends},
                            {"seq_starts", seq_starts, size_t(n_seq + 1) * 4}},
-                          {{"h", h, rows * 4}, {"h_last", h_last, ends}}, nullptr)));
-    TRY(check_workspace(workspace, workspace_bytes, glr_ws_bytes(false, T, n_seq, D)));
+                          {{"h", h, rows * 4}, {"h_last", h_last, ends}}, nullptr, {"workspace", workspace, need})));
+    TRY(check_workspace(workspace, workspace_bytes, need));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     GlrParams p = {};
     p.rate = rate;
@@ -426,11 +434,13 @@ pararnn_status pararnn_glr_adjoint(const void* u, pararnn_dtype u_dtype, const f
     TRY(check_ptr(dh0, "dh0", false));
     TRY(glr_shape(T, n_seq, D, seq_starts));
     const size_t rows = size_t(T) * D, ends = size_t(n_seq) * D * 4;
+    const size_t need = glr_ws_bytes(true, T, n_seq, D);
     TRY((check_apart<7, 3>({{"u", u, rows * 3 * dtype_bytes(u_dtype)}, {"rate", rate, size_t(D) * 4}, {"h0", h0, ends},
                            {"seq_starts", seq_starts, size_t(n_seq + 1) * 4}, {"h", h, rows * 4}, {"dh", dh, rows * 4},
                            {"dh_last", dh_last, ends}},
-                          {{"du", du, rows * 12}, {"drate", drate, size_t(D) * 4}, {"dh0", dh0, ends}}, nullptr)));
-    TRY(check_workspace(workspace, workspace_bytes, glr_ws_bytes(true, T, n_seq, D)));
+                          {{"du", du, rows * 12}, {"drate", drate, size_t(D) * 4}, {"dh0", dh0, ends}}, nullptr,
+                          {"workspace", workspace, need})));
+    TRY(check_workspace(workspace, workspace_bytes, need));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     GlrParams p = {};
     p.rate = rate;
@@ -547,10 +557,12 @@ pararnn_status pararnn_rms_norm_adjoint(const void* dy, pararnn_dtype dy_dtype, 
     NormShape s;
     TRY(norm_shape(T, D, kNormAdjVecs, &s));
     const size_t n = size_t(T) * D, es = dtype_bytes(sum_dtype);
+    const size_t need = align256(size_t(norm_adjoint_parts(T, s)) * D * 4);
     TRY((check_apart<5, 2>({{"dy", dy, n * dtype_bytes(dy_dtype)}, {"sum", sum, n * es}, {"w", w, size_t(D) * 4},
                            {"rstd", rstd, size_t(T) * 4}, {"dsum", dsum, n * es}},
-                          {{"dx", dx, n * es}, {"dw", dw, size_t(D) * 4}}, dsum && dsum == dx ? dsum : nullptr)));
-    TRY(check_workspace(workspace, workspace_bytes, align256(size_t(norm_adjoint_parts(T, s)) * D * 4)));
+                          {{"dx", dx, n * es}, {"dw", dw, size_t(D) * 4}}, dsum && dsum == dx ? dsum : nullptr,
+                          {"workspace", workspace, need})));
+    TRY(check_workspace(workspace, workspace_bytes, need));
     NormAdjParams p;
     p.dy = dy;
     p.v = sum;
@@ -630,7 +642,8 @@ pararnn_status pararnn_fp8_project(const void* x, const float* x_scale, const vo
     const long long KB = blocks128(K);
     TRY((check_apart<5, 1>({{"x", x, size_t(M) * K}, {"x_scale", x_scale, size_t(M) * KB * 4}, {"w", w, size_t(N) * K},
                             {"w_scale", w_scale, size_t(blocks128(N)) * KB * 4}, {"bias", bias, size_t(N) * 4}},
-                           {{"u", u, size_t(M) * N * dtype_bytes(u_dtype)}}, nullptr)));
+                           {{"u", u, size_t(M) * N * dtype_bytes(u_dtype)}}, nullptr,
+                           {"workspace", workspace, sizeof(WsHeader)})));
     TRY(check_workspace(workspace, workspace_bytes, sizeof(WsHeader)));
     int sms = 0;
     TRY(device_info(&sms));

@@ -47,3 +47,30 @@ def test_workspace_with_gaps(capi):
     for call in calls(capi)[0]:
         with pytest.raises(ValueError, match="workspace"):
             call(workspace=torch.empty(2, 1 << 16, dtype=torch.uint8)[:, ::2])
+
+
+def test_workspace_that_overlaps_an_array(capi):
+    """The workspace is written, so it may meet no array of the call."""
+    def scan(ws, starts=None):
+        return capi.lib.pararnn_glr_scan(A[0], 1, A[1], A[2], starts, A[9], A[3], 8, 2, 16, ws, 1 << 19, None)
+
+    def adjoint(ws):
+        return capi.lib.pararnn_glr_adjoint(A[0], 0, A[1], A[2], A[8], A[3], A[4], A[5], A[6], A[7], A[9], 8, 2, 16, ws,
+                                            1 << 19, None)
+
+    def norm(ws):
+        return capi.lib.pararnn_rms_norm_adjoint(A[0], 1, A[1], 1, A[2], A[3], A[4], A[5], A[6], 4, 32, ws, 1 << 19, None)
+
+    def project(ws):
+        return capi.lib.pararnn_fp8_project(A[0], A[1], A[2], A[3], A[4], A[5], 1, 4, 16, 32, ws, 1 << 19, None)
+
+    for call, arrays in ((scan, (0, 1, 2, 3, 9)), (adjoint, range(10)), (norm, range(7)), (project, range(6))):
+        for k in arrays:
+            assert call(A[k]) == capi.ERR_INVALID_ARG, (call.__name__, k)
+            assert "workspace" in capi.last_error()
+    assert scan(A[8], starts=A[8]) == capi.ERR_INVALID_ARG
+    # beside every array: nothing to refuse (without a GPU the call then fails there;
+    # with one it would run on these addresses)
+    if not torch.cuda.is_available():
+        for call in (scan, adjoint, norm, project):
+            assert call(A[12]) == capi.ERR_CUDA, call.__name__
