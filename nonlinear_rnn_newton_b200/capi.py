@@ -736,6 +736,14 @@ def _code(dtype, name, codes):
     return code
 
 
+def _on(stream, device):
+    """The context of a given stream, which has to be one of the tensors'
+    device: a call runs on that device's current stream."""
+    if stream.device != device:
+        raise ValueError(f"stream must be one of {device}, is one of {stream.device}")
+    return torch.cuda.stream(stream)
+
+
 def _address(t):
     return None if t is None else t.data_ptr()
 
@@ -807,7 +815,7 @@ def pararnn_glr_scan(u, rate, h0=None, seq_starts=None, h=None, h_last=None, wan
     [T,D], h_last [n_seq,D] or None).  Rows in no sequence are not written: in
     an h made here they hold anything.  Asynchronous on the stream."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, u.device):
             return pararnn_glr_scan(u, rate, h0, seq_starts, h, h_last, want_last, workspace)
     shape, T, n_seq, D = _glr_args(u, rate, h0, seq_starts)
     dev = u.device
@@ -831,7 +839,7 @@ def pararnn_glr_adjoint(u, rate, h0, h, dh, dh_last=None, seq_starts=None, du=No
     None).  Returns (du as u in fp32, drate [D], dh0 [n_seq,D] or None).
     Asynchronous on the stream."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, u.device):
             return pararnn_glr_adjoint(u, rate, h0, h, dh, dh_last, seq_starts, du, drate, dh0, want_dh0,
                                        workspace)
     shape, T, n_seq, D = _glr_args(u, rate, h0, seq_starts)
@@ -863,7 +871,7 @@ def pararnn_glr_step(u, rate, h_prev=None, h_next=None, stream=None):
     """One step for B sequences: u [B,3,D], h_prev [B,D] (None = zeros).
     h_next may be h_prev itself (in place); a new tensor if None."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, u.device):
             return pararnn_glr_step(u, rate, h_prev, h_next)
     if u.dim() != 3 or u.shape[1] != 3:
         raise ValueError(f"u must be [B,3,D], got shape {tuple(u.shape)}")
@@ -899,7 +907,7 @@ def pararnn_rms_norm(x, w, residual=None, eps=1e-6, out_dtype=torch.bfloat16, su
     the residual's type (None without a residual), rstd [...]).  sum may be
     the residual itself (in place)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x.device):
             return pararnn_rms_norm(x, w, residual, eps, out_dtype, sum, y, y_scale, rstd)
     T, D = _rows(x, "x")
     dev, shape = x.device, x.shape
@@ -950,7 +958,7 @@ def pararnn_rms_norm_adjoint(dy, sum, w, rstd, dsum=None, dx=None, dw=None, work
     sum's type, the gradient of x and residual alike, dw [D] fp32).  dx may be
     dsum itself."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, sum.device):
             return pararnn_rms_norm_adjoint(dy, sum, w, rstd, dsum, dx, dw, workspace)
     T, D = _rows(sum, "sum")
     dev, shape = sum.device, sum.shape
@@ -981,7 +989,7 @@ def pararnn_fp8_quantize(x, block_rows=1, q=None, scale=None, stream=None):
     columns (block_rows = 1, scale [..., ceil(K/128)]) or per 128 rows and 128
     columns (block_rows = 128, x [N,K], scale [ceil(N/128), ceil(K/128)])."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x.device):
             return pararnn_fp8_quantize(x, block_rows, q, scale)
     M, K = _rows(x, "x")
     dev, shape = x.device, x.shape
@@ -1018,7 +1026,7 @@ def pararnn_fp8_project(x, x_scale, w, w_scale, bias=None, out_dtype=torch.bfloa
     their scales (pararnn_rms_norm or pararnn_fp8_quantize), bias [N] fp32 or
     None.  Returns u [..., N] in out_dtype (bf16 or fp32)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x.device):
             return pararnn_fp8_project(x, x_scale, w, w_scale, bias, out_dtype, u, workspace)
     M, K = _rows(x, "x")
     dev, shape = x.device, x.shape

@@ -74,3 +74,11 @@ def test_workspace_that_overlaps_an_array(capi):
     if not torch.cuda.is_available():
         for call in (scan, adjoint, norm, project):
             assert call(A[12]) == capi.ERR_CUDA, call.__name__
+
+
+def test_stream_of_another_device(capi):
+    """The call would otherwise run on the current stream of the tensors' device."""
+    stream = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0, device_index=1)
+    for call in sum(calls(capi), []):
+        with pytest.raises(ValueError, match="stream must be one of"):
+            call(stream=stream)
