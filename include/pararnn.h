@@ -677,7 +677,9 @@ PARARNN_API uint64_t pararnn_kernel_launch_count(void);
  *   which = 1: the grid barrier (one CTA of a cooperative launch never
  *              arrives);
  *   which = 2: the barrier waits of the layer operators (nothing arrives;
- *              their limit is counted in SM clocks, two a nanosecond).
+ *              their limit is counted in SM clocks, two a nanosecond);
+ *   which = 3: the gated recurrence's look at other CTAs' tiles (nothing is
+ *              published; the limit likewise).
  * The wait must give up after `limit_ns` nanoseconds and the call must return
  * PARARNN_ERR_TIMEOUT with the context still usable.  Needs a workspace of
  * at least 16384 bytes.  Synchronous. */

@@ -313,6 +313,33 @@ __device__ __forceinline__ void glr_publish(const GlrParams& p, const GlrShared<
                  : "memory");
 }
 
+// Maps of `cnt` tiles (as many as eight are taken), `step` apart, once all of
+// them are there.  False when the wait ran out.
+__device__ __forceinline__ bool look_up(const uint4* from, size_t step, int cnt, uint4 (&v)[8], int* err, uint64_t limit_ns)
+{
+    long long t0 = 0;
+    for (;;) {
+        bool there = true;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = j < cnt ? ld_map(from + j * step) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) there = there && v[j].x != ~0u && v[j].y != ~0u && v[j].z != ~0u && v[j].w != ~0u;
+        if (__all_sync(0xffffffffu, there)) return true;
+        if (t0 == 0) t0 = clock64();
+        if (__any_sync(0xffffffffu, clock64() - t0 > (long long)(2 * limit_ns))) {
+            raise_error(err, PARARNN_ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// Self test: a look at maps that nobody publishes gives up.
+__global__ void selftest_look_up_kernel(const uint4* maps, int* err, unsigned long long limit_ns)
+{
+    uint4 v[8];
+    look_up(maps + threadIdx.x, 32, 3, v, err, limit_ns);
+}
+
 // Then the state entering tile k, from the one the CTA's tile before ended with
 // (the other control warp passes it on), and from it the state entering each
 // warp's rows.  False when a wait ran out.
@@ -325,22 +352,7 @@ __device__ __forceinline__ bool glr_carry(const GlrParams& p, GlrShared<W, NS>& 
     Map2 all{both(1.f), both(0.f), false};
     for (int i = 0; i < cnt; i += 8) {
         uint4 v[8];
-        long long t0 = 0;
-        for (;;) {
-            bool there = true;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = i + j < cnt ? ld_map(from + size_t(i + j) * p.S * 32) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                there = there && v[j].x != ~0u && v[j].y != ~0u && v[j].z != ~0u && v[j].w != ~0u;
-            if (__all_sync(0xffffffffu, there)) break;
-            if (t0 == 0) t0 = clock64();
-            const bool late = clock64() - t0 > (long long)(2 * p.wait_ns);
-            if (__any_sync(0xffffffffu, late)) {
-                raise_error(&p.hdr->error, PARARNN_ERR_TIMEOUT);
-                return false;
-            }
-        }
+        if (!look_up(from + size_t(i) * p.S * 32, size_t(p.S) * 32, cnt - i, v, &p.hdr->error, p.wait_ns)) return false;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             if (i + j < cnt) {

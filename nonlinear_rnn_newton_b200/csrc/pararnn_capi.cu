@@ -29,6 +29,7 @@
 #include "linear_scan.cuh"
 #include "project.cuh"
 #include "fp8.cuh"
+#include "glr.cuh"
 
 using namespace pararnn;
 
@@ -990,7 +991,7 @@ pararnn_status linear_scan_async(const void* u, pararnn_dtype dt, const float* h
 pararnn_status selftest_wait_timeout(int which, long long limit_ns, void* ws, size_t ws_bytes, cudaStream_t stream)
 {
     t_err[0] = '\0';
-    if (which < 0 || which > 2) return fail(PARARNN_ERR_INVALID_ARG, "which must be 0, 1 or 2");
+    if (which < 0 || which > 3) return fail(PARARNN_ERR_INVALID_ARG, "which must be 0, 1, 2 or 3");
     if (limit_ns <= 0 || limit_ns > 10000000000ll) return fail(PARARNN_ERR_INVALID_ARG, "limit_ns out of range");
     TRY(check_workspace(ws, ws_bytes, kSelftestWorkspace));
     CUDA_TRY(cudaMemsetAsync(ws, 0, kSelftestWorkspace, stream));
@@ -1003,6 +1004,10 @@ pararnn_status selftest_wait_timeout(int which, long long limit_ns, void* ws, si
         CUDA_TRY(cudaGetLastError());
     } else if (which == 2) {
         selftest_clocked_wait_kernel<<<1, 32, 0, stream>>>(&hdr->error, lim);
+        CUDA_TRY(cudaGetLastError());
+    } else if (which == 3) {
+        CUDA_TRY(cudaMemsetAsync(desc, 0xff, 3 * 512, stream));  // three tiles' maps, not there
+        selftest_look_up_kernel<<<1, 32, 0, stream>>>(reinterpret_cast<const uint4*>(desc), &hdr->error, lim);
         CUDA_TRY(cudaGetLastError());
     } else {
         int sms = 0;

@@ -203,3 +203,12 @@ def test_rate_gradient_of_many_equal_rows(cuda):
     assert torch.equal(dh0, one[:, 0])
     want = -T * O.sigmoid(C.f64(r))
     near(drate, want, (2 * np.abs(C.f64(r)) + 7 + 2 + 43) * C.EPS * np.abs(want), "drate")
+
+
+def test_look_up_gives_up(cuda):
+    """The wait for other CTAs' tiles ends by itself and is reported."""
+    from nonlinear_rnn_newton_b200 import capi
+    ws = torch.zeros(16384, dtype=torch.uint8, device=cuda)
+    assert P().pararnn_selftest_wait_timeout(3, 5_000_000, ws) == capi.ERR_TIMEOUT
+    torch.zeros(1, device=cuda).add_(1)
+    torch.cuda.synchronize()  # the context is still usable
