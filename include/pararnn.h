@@ -514,7 +514,7 @@ PARARNN_API pararnn_status pararnn_lstm_step(const void* u, pararnn_dtype u_dtyp
  * and workspaces, here and below, must not overlap inputs or each other.
  * Asynchronous on `stream`, capturable in a CUDA graph; a device-side failure
  * (a bounded wait that ran out) is reported by pararnn_read_result on the same
- * workspace.  Calls that
+ * workspace, and by pararnn_take_failure.  Calls that
  * may run at the same time need workspaces of their own. */
 PARARNN_API size_t pararnn_glr_workspace_size(int64_t T, int64_t n_seq, int64_t D);
 PARARNN_API pararnn_status pararnn_glr_scan(const void* u, pararnn_dtype u_dtype, const float* rate,
@@ -627,13 +627,22 @@ PARARNN_API pararnn_status pararnn_fp8_quantize(const void* x, pararnn_dtype x_d
  *           scans and the decode steps
  * K a multiple of 16, N a multiple of 8 (else UNSUPPORTED).  Asynchronous on
  * `stream`; a device-side failure (a bounded wait that ran out) is reported
- * by pararnn_read_result on the same workspace. */
+ * by pararnn_read_result on the same workspace, and by pararnn_take_failure. */
 PARARNN_API size_t pararnn_fp8_project_workspace_size(int64_t M, int64_t N, int64_t K);
 PARARNN_API pararnn_status pararnn_fp8_project(const void* x, const float* x_scale, const void* w,
                                                const float* w_scale, const float* bias, void* u,
                                                pararnn_dtype u_dtype, int64_t M, int64_t N, int64_t K,
                                                void* workspace, size_t workspace_bytes,
                                                pararnn_stream_t stream);
+
+/* Whether a bounded wait of pararnn_glr_scan, pararnn_glr_adjoint or
+ * pararnn_fp8_project has run out on the current device since the last look,
+ * whatever the workspace: PARARNN_OK, or the failure's status once
+ * (PARARNN_ERR_TIMEOUT; the outputs of a call since the last look are then not
+ * valid).  For callers that keep no workspaces: look where the results are
+ * waited for.  Synchronises `stream`; calls on other streams count once they
+ * are done.  Not within a graph's capture. */
+PARARNN_API pararnn_status pararnn_take_failure(pararnn_stream_t stream);
 
 /* ------------------------------------------------------------- baselines */
 
@@ -681,7 +690,8 @@ PARARNN_API uint64_t pararnn_kernel_launch_count(void);
  *   which = 3: the gated recurrence's look at other CTAs' tiles (nothing is
  *              published; the limit likewise).
  * The wait must give up after `limit_ns` nanoseconds and the call must return
- * PARARNN_ERR_TIMEOUT with the context still usable.  Needs a workspace of
+ * PARARNN_ERR_TIMEOUT with the context still usable (pararnn_take_failure then
+ * tells of 2 and 3 as of any other).  Needs a workspace of
  * at least 16384 bytes.  Synchronous. */
 PARARNN_API pararnn_status pararnn_selftest_wait_timeout(int which, int64_t limit_ns, void* workspace,
                                              size_t workspace_bytes, pararnn_stream_t stream);

@@ -65,6 +65,7 @@ __all__ = [
     "pararnn_rms_norm_adjoint",
     "pararnn_rms_norm_adjoint_workspace_size",
     "pararnn_selftest_wait_timeout",
+    "pararnn_take_failure",
 ]
 
 

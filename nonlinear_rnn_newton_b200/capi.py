@@ -121,6 +121,7 @@ SIGNATURES = {
     "pararnn_fp8_quantize": (_st, [_vp, _st, ctypes.c_int, _vp, _vp, _i64, _i64, _vp]),
     "pararnn_fp8_project_workspace_size": (ctypes.c_size_t, [_i64, _i64, _i64]),
     "pararnn_fp8_project": (_st, [_vp, _vp, _vp, _vp, _vp, _vp, _st, _i64, _i64, _i64, _vp, ctypes.c_size_t, _vp]),
+    "pararnn_take_failure": (_st, [_vp]),
     "pararnn_status_string": (ctypes.c_char_p, [_st]),
     "pararnn_last_error": (ctypes.c_char_p, []),
     "pararnn_version": (ctypes.c_char_p, []),
@@ -773,6 +774,15 @@ def _space(near, workspace, size, *shape):
     elif workspace.device != near.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {near.device}, is on {workspace.device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def pararnn_take_failure(device=None, stream=None):
+    """Raises PararnnError (ERR_TIMEOUT) if a bounded wait of the scan, its
+    adjoint or the 8-bit product has run out on the device (the current one)
+    since the last look, whoever kept the workspace.  Waits for the stream; call
+    it where results are waited for."""
+    with torch.cuda.device(device):
+        _check(lib.pararnn_take_failure(_stream(device, stream)), allow=(OK,))
 
 
 def pararnn_glr_workspace_size(T, n_seq, D):

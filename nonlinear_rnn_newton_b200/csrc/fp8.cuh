@@ -141,20 +141,6 @@ __device__ __forceinline__ bool mbar_wait_clocked(uint64_t* bar, uint32_t parity
     }
 }
 
-// Self test: a wait on a barrier that nothing arrives on gives up.
-__global__ void selftest_clocked_wait_kernel(int* err, unsigned long long limit_ns)
-{
-    __shared__ uint64_t bar;
-    if (threadIdx.x == 0) {
-        mbar_init(&bar, 1);
-        fence_mbar_init();
-    }
-    __syncthreads();
-    mbar_wait_clocked(&bar, 0, err, limit_ns);
-    __syncthreads();
-    if (threadIdx.x == 0) mbar_inval(&bar);
-}
-
 // A tiled load into this CTA's shared memory that completes on a barrier of
 // either CTA of the pair (no multicast).
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* tm, int c0, int c1, uint32_t bar)
@@ -166,12 +152,32 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* t
         : "memory");
 }
 
-// After a wait that ran out: give the copies in flight into this CTA's shared
-// memory time to land (a copy takes microseconds) before the CTA ends.
-__device__ __forceinline__ void let_copies_land()
+// Whether a wait of a layer operator has run out on this device since the host
+// last asked: callers may drop the workspace that holds a call's own outcome.
+__device__ int g_layer_failure = 0;
+
+// After a wait that ran out: mark the device, and give the copies in flight into
+// this CTA's shared memory time to land (a copy takes microseconds) before the
+// CTA ends.
+__device__ __forceinline__ void give_up()
 {
+    raise_error(&g_layer_failure, PARARNN_ERR_TIMEOUT);
     const uint64_t t0 = global_timer_ns();
     while (global_timer_ns() - t0 < 2000000ull) __nanosleep(1000);
+}
+
+// Self test: a wait on a barrier that nothing arrives on gives up.
+__global__ void selftest_clocked_wait_kernel(int* err, unsigned long long limit_ns)
+{
+    __shared__ uint64_t bar;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    if (!mbar_wait_clocked(&bar, 0, err, limit_ns)) give_up();
+    __syncthreads();
+    if (threadIdx.x == 0) mbar_inval(&bar);
 }
 
 // 16 consecutive fp32 columns of this warp's 32 TMEM lanes (one per thread)
@@ -440,7 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kQThreads, 1)
         }
         if (lane == 0) tma_store_wait_read();
     }
-    if (!ok) let_copies_land();
+    if (!ok) give_up();
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();
@@ -601,7 +607,7 @@ __global__ void __launch_bounds__(kNThreads)
             for (int j = 0; j < NT; ++j) red[j * 128 + 32 * lq + lane] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
         }
     }
-    if (!ok) let_copies_land();
+    if (!ok) give_up();
     tc_fence_before();
     __syncthreads();
     if (w == 1) tmem_dealloc_cg<1>(tmem, LY::tmem_cols);

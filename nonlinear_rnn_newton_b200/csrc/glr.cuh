@@ -337,7 +337,7 @@ __device__ __forceinline__ bool look_up(const uint4* from, size_t step, int cnt,
 __global__ void selftest_look_up_kernel(const uint4* maps, int* err, unsigned long long limit_ns)
 {
     uint4 v[8];
-    look_up(maps + threadIdx.x, 32, 3, v, err, limit_ns);
+    if (!look_up(maps + threadIdx.x, 32, 3, v, err, limit_ns)) give_up();
 }
 
 // Then the state entering tile k, from the one the CTA's tile before ended with
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(GlrScanLayout<UT>::kThreads, 1)
         }
         copy_empty<W>(p.starts, p.T, p.n_seq, p.D, p.h0, p.h_last);
     }
-    if (!ok) let_copies_land();
+    if (!ok) give_up();
 }
 
 template <class UT>
@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
         }
         copy_empty<W>(p.starts, p.T, p.n_seq, p.D, p.dh_last, p.dh0);
     }
-    if (!ok) let_copies_land();
+    if (!ok) give_up();
     // this CTA's part of the rates' gradients, the warps in order
     __syncthreads();
     if (w < W) sh.enter[0][w][lane] = neg(nds);

@@ -378,6 +378,21 @@ pararnn_status launch_wide(const uint8_t* x, const uint8_t* w, Fp8Params p, int 
 
 extern "C" {
 
+pararnn_status pararnn_take_failure(pararnn_stream_t stream)
+{
+    t_err[0] = '\0';
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    void* at = nullptr;
+    int code = 0;
+    CUDA_TRY(cudaGetSymbolAddress(&at, g_layer_failure));
+    CUDA_TRY(cudaMemcpyAsync(&code, at, sizeof(code), cudaMemcpyDeviceToHost, st));
+    CUDA_TRY(cudaStreamSynchronize(st));
+    if (code == 0) return PARARNN_OK;
+    CUDA_TRY(cudaMemsetAsync(at, 0, sizeof(code), st));
+    CUDA_TRY(cudaStreamSynchronize(st));
+    return fail(pararnn_status(code), "a bounded wait of a layer operator ran out since the last look: its outputs are not valid");
+}
+
 size_t pararnn_glr_workspace_size(int64_t T, int64_t n_seq, int64_t D) { return glr_ws_bytes(false, T, n_seq, D); }
 size_t pararnn_glr_adjoint_workspace_size(int64_t T, int64_t n_seq, int64_t D) { return glr_ws_bytes(true, T, n_seq, D); }
 

@@ -212,3 +212,25 @@ def test_look_up_gives_up(cuda):
     assert P().pararnn_selftest_wait_timeout(3, 5_000_000, ws) == capi.ERR_TIMEOUT
     torch.zeros(1, device=cuda).add_(1)
     torch.cuda.synchronize()  # the context is still usable
+
+
+@pytest.mark.parametrize("which", [2, 3])
+def test_failures_are_seen_without_a_workspace(cuda, which):
+    """A wait that ran out is told once, by a look that knows no workspace, and
+    the calls after it are as before."""
+    from nonlinear_rnn_newton_b200 import capi
+    u, rate, h0, starts = C.glr_inputs(600, 1, 64, BF16, 0)
+    call = lambda: P().pararnn_glr_scan(u[None].to(cuda), rate.to(cuda), h0.to(cuda))[0]
+    want = call()
+    try:
+        P().pararnn_take_failure()  # whatever came before
+    except capi.PararnnError:
+        pass
+    P().pararnn_take_failure(cuda)
+    ws = torch.zeros(16384, dtype=torch.uint8, device=cuda)
+    assert P().pararnn_selftest_wait_timeout(which, 5_000_000, ws) == capi.ERR_TIMEOUT
+    with pytest.raises(capi.PararnnError) as e:
+        P().pararnn_take_failure()
+    assert e.value.status == capi.ERR_TIMEOUT
+    assert torch.equal(call(), want)
+    P().pararnn_take_failure(stream=torch.cuda.Stream())

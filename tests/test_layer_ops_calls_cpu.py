@@ -82,3 +82,9 @@ def test_stream_of_another_device(capi):
     for call in sum(calls(capi), []):
         with pytest.raises(ValueError, match="stream must be one of"):
             call(stream=stream)
+
+
+def test_failures_cannot_be_asked_for_without_a_device(capi):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    assert capi.lib.pararnn_take_failure(None) == capi.ERR_CUDA
