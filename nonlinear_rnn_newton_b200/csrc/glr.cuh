@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(GlrScanLayout<UT>::kThreads, 1)
         float2 a[NS][R], b[NS][R];
         RowMasks rm[NS];
         if (mine > 0) fold(0, a[0], b[0], rm[0]);
-        if (ahead > 1 && mine > 1) fold(1, a[1], b[1], rm[1]);
+        if (ahead > 1 && mine > 1 && ok) fold(1, a[1], b[1], rm[1]);
         for (int n = 0; n < mine && ok; n += NS) {
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
         float2 sr[NS][R], up[NS][R];
         RowMasks rm[NS];
         if (mine > 0) fold(0, sr[0], up[0], rm[0]);
-        if (ahead > 1 && mine > 1) fold(1, sr[1], up[1], rm[1]);
+        if (ahead > 1 && mine > 1 && ok) fold(1, sr[1], up[1], rm[1]);
         for (int n = 0; n < mine && ok; n += NS) {
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
