@@ -11,10 +11,7 @@
 // Both are bound by HBM: a row is read once into registers (8 columns a
 // vector, NV vectors a thread) and everything else happens there.  A row
 // belongs to `tpr` threads (a multiple of 32); 16 neighbouring lanes hold one
-// block of 128 columns, so its scale needs four shuffles.  The norm of T 32768
-// D 2048 (fp32 in, bf16 residual, e4m3 out) takes 98 to 100 us, 6.1 TB/s: 96 with
-// a product by the scale's rounded reciprocal for the quotient, which puts
-// values beside a middle on its other side.
+// block of 128 columns, so its scale needs four shuffles.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -199,8 +196,12 @@ struct NormParams {
     int y_dtype;
 };
 
+// T 32768 D 2048 (fp32 in, bf16 residual, e4m3 out): 96 us, 6.3 TB/s, from a
+// graph; with a product by the scale's rounded reciprocal for the quotient the
+// same.  48 registers let ten CTAs of 128 threads on an SM; the quotients took
+// 50, nine CTAs and 98 us (T 16384 D 4096: 106.5 against 98).
 template <class XT, class RT, int NV>
-__global__ void __launch_bounds__(kNormThreads) rms_norm_kernel(const NormParams p)
+__global__ void __maxnreg__(NV <= 2 ? 48 : 128) rms_norm_kernel(const NormParams p)
 {
     __shared__ float s_red[32];
     const int tpr = p.tpr, rows = blockDim.x / tpr;
