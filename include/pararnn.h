@@ -568,7 +568,9 @@ PARARNN_API pararnn_status pararnn_glr_step(const void* u, pararnn_dtype u_dtype
  *            makes of an fp32 y.  A block that holds NaN or infinity stands
  *            for NaN throughout.
  *   rstd     [T] fp32 out for the adjoint, or NULL
- * y and the scales come from the unrounded v.  D a multiple of 8 (16 for
+ * y and the scales come from the unrounded v.  The mean of v^2 is formed in
+ * fp32: a row whose squares add up to more than fp32 holds (|v| of 1e19 and
+ * above) has rstd 0, one of less than 1e-19 or so eps alone.  D a multiple of 8 (16 for
  * e4m3) and at most 16384, else UNSUPPORTED.  Other overlaps of outputs are
  * refused.  Asynchronous on `stream`, no workspace. */
 PARARNN_API pararnn_status pararnn_rms_norm(const void* x, pararnn_dtype x_dtype, const void* residual,

@@ -64,7 +64,9 @@ struct Decay2 {
 // nrate: the rates' negatives.  Near: every rate of the warp is below 1/8, so l <=
 // rate is too and the far branch (with its special-function use) is left out.
 // Loops over rows are built for both: a branch in each row would keep the rows'
-// arithmetic from overlapping.  The far branch takes a from the exponential
+// arithmetic from overlapping.  One fast channel makes its slab's warps take the
+// far branch: scan B8 L4096 D1024 95 against 88 us, adjoint B4 L8192 D2048 355
+// against 309.  The far branch takes a from the exponential
 // itself: 1 + (a - 1) would keep only the bits of a small a above 2^-24, and the
 // gradients of fast decays are multiples of a.
 template <bool Near>

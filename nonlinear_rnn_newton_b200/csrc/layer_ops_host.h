@@ -194,7 +194,7 @@ pararnn_status launch_glr_adjoint(const UT* u, GlrParams p, float* drate, long l
 // Vectors of 8 columns a thread keeps: two (more where D needs it).  Measured at
 // T 32768 D 2048, norm: two 92 us, four 96; adjoint: two 98 us, one 108.
 constexpr int kNormVecs = 2, kNormAdjVecs = 2;
-constexpr int kNormMaxParts = 148 * 8;  // most CTAs of the adjoint
+constexpr int kNormMaxParts = 148 * 8;  // most CTAs of the adjoint: eight on each of a B200's 148 SMs
 
 struct NormShape {
     int tpr, nv, threads, rows;
@@ -212,7 +212,7 @@ pararnn_status norm_shape(long long T, long long D, int vectors, NormShape* s)
     // the fewest threads a row that keep it within `vectors` vectors each
     int tpr = 32;
     while (tpr < kNormThreads && tpr * vectors < d8) tpr *= 2;
-    // with few rows the chip is far from full: spread each over more threads
+    // with few rows the chip (148 SMs) is far from full: spread each over more threads
     while (tpr < kNormThreads && tpr < d8 && T * tpr < 148 * 512) tpr *= 2;
     s->tpr = tpr;
     s->nv = 1;
@@ -332,7 +332,7 @@ pararnn_status launch_clusters(K kern, int grid, int threads, int cluster, size_
 }
 
 // How many CTAs of the narrow form share a tile's blocks of K: as long as all
-// of them run at once (two an SM, less what clusters of up to eight leave over:
+// of them run at once (two on each of 148 SMs, less what clusters of up to eight leave over:
 // 288 in clusters of four took two rounds, 256 one).
 constexpr long long kNarrowRoom = 256;
 
@@ -676,11 +676,15 @@ pararnn_status pararnn_fp8_project(const void* x, const float* x_scale, const vo
     p.wait_ns = kWaitLimitNs;
     const uint8_t *xb = static_cast<const uint8_t*>(x), *wb = static_cast<const uint8_t*>(w);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-        // Blocks of K one after another in the fullest CTA, and what one costs: a
+    // Blocks of K one after another in the fullest CTA, and what one costs: a
     // pair's 0.53 us each and 5.5 us before and after, the narrow form's (64
-    // rows) 0.65 and 6.  N 6144 K 2048: 12.6 (narrow) against 14.2 us at M 128,
-    // 15.8 against 14.4 at M 200; N 2048 K 8192: 25.9 against 39.7 at M 512,
-    // 43.0 against 40.0 at M 768.
+    // rows) 0.65 and 6.  Both forms were measured at eleven M from 65 to 4096 for
+    // ten weights from N 64 K 2048 to N 12288 K 4096, bf16 and fp32 out: what is
+    // chosen is the faster one or within 8 % of it, but for M 512 N 1304 K 512
+    // (narrow 9.4 us, wide 8.1).  N 6144 K 2048: 12.6 (narrow) against 14.2 us at
+    // M 128, 16.5 against 14.2 at M 256; N 2048 K 8192: 25.9 against 39.3 at
+    // M 512, 43.0 against 39.6 at M 768; N 264 K 1104: 9.2 against 10.9 at M 1024,
+    // 13.2 against 10.9 at M 4096; N 2048 K 128: 8.0 against 6.0 at M 65.
     const long long pairs = std::max(1, sms / 2);
     const long long wide_tiles = (M + 2 * kQM - 1) / (2 * kQM) * ((N + kQN - 1) / kQN);
     const long long tiles = (M + 63) / 64 * blocks128(N);

@@ -274,9 +274,12 @@ struct NormAdjParams {
 
 // A CTA takes rows blockIdx.x * rows + k * gridDim.x * rows, and asks for its
 // next row before it works on this one; dw of its rows stays in registers and
-// leaves once, one row of `part` a CTA.  T 32768 D 2048, bf16: 94 us, 5.7 TB/s
-// (without the loads ahead 120 us, one vector a thread 108); 119 registers
-// leave four CTAs an SM, whose loads of three arrays are 48 KB in flight.
+// leaves once, one row of `part` a CTA.  T 32768 D 2048, bf16: 94 to 96 us, 5.6
+// TB/s (without the loads ahead 120 us, one vector a thread 108); 125 registers
+// leave four CTAs an SM, whose loads of three arrays are 48 KB in flight.  Four
+// vectors a thread (D above 8192) do not fit into the 128 registers that 512
+// threads leave: T 4096 D 16384 takes 172 us in bf16 (540 bytes of spills read a
+// thread) and 458 in fp32 (1236), where 82 and 164 are the memory's.
 template <class YT, class VT, int NV>
 __global__ void __launch_bounds__(kNormThreads) rms_norm_adjoint_kernel(const NormAdjParams p)
 {
