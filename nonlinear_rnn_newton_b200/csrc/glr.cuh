@@ -727,6 +727,8 @@ __global__ void __launch_bounds__(GlrAdjointLayout<UT>::kThreads, 1)
             if (lane == 0) mbar_arrive(&sh.empty[s]);
             const float2 y = __fadd2_rn(tile_nds, neg(rest)), all = __fadd2_rn(nds, y);
             rest = __fadd2_rn(__fadd2_rn(all, neg(nds)), neg(y));
+            // an infinite sum stays one: what is left of it is no number
+            rest = make_float2(fabsf(all.x) <= 3.4e38f ? rest.x : 0.f, fabsf(all.y) <= 3.4e38f ? rest.y : 0.f);
             nds = all;
         };
         float2 sr[NS][R], up[NS][R];

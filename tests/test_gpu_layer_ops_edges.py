@@ -234,3 +234,19 @@ def test_failures_are_seen_without_a_workspace(cuda, which):
     assert e.value.status == capi.ERR_TIMEOUT
     assert torch.equal(call(), want)
     P().pararnn_take_failure(stream=torch.cuda.Stream())
+
+
+def test_infinite_rate_gradients_stay_infinite(cuda):
+    """One infinite gradient, and rows that all add to drate with one sign:
+    it is infinite and not NaN, and other channels do not notice."""
+    T, D = 3000, 72
+    u = torch.randn(1, T, 3, D, device=cuda)
+    u[:, :, 2] = -1
+    rate, h = 0.05 + 0.1 * torch.rand(D, device=cuda), torch.ones(1, T, D, device=cuda)
+    dh = torch.ones(1, T, D, device=cuda)
+    want = P().pararnn_glr_adjoint(u, rate, h[:, 0].contiguous(), h, dh)[1]
+    dh[0, 1700, 5] = float("inf")
+    got = P().pararnn_glr_adjoint(u, rate, h[:, 0].contiguous(), h, dh)[1]
+    assert got[5] == -float("inf")
+    got[5] = want[5]
+    assert torch.equal(got, want) and torch.isfinite(want).all()
